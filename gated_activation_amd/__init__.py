@@ -16,6 +16,17 @@ is not built, importing this package raises: there is no fallback.
     gelu_and_mul(x, approximate)        x: [T, 2d] -> [T, d] (tanh or erf GELU)
     squared_relu_bounded(x, live_rows)  x: [M, d]  -> [M, d] (live rows only)
     z_from_sparsity(p)                  Phi^-1(p), host-side
+
+Training (no autograd graph: each backward is its own call):
+
+    activation_checkpoint(x, activation)        -> out, Checkpoint (x kept in 8 bits)
+    activation_backward(dout, kept, activation) kept: the Checkpoint or x -> dx
+    checkpoint_store(x), checkpoint_restore(checkpoint, dtype)
+    layer_norm(x, weight, bias)                 -> y, stats
+    layer_norm_checkpoint(x, weight, bias)      -> y, Checkpoint (x - mean in 8 bits)
+    layer_norm_backward(dy, kept, weight, stats) -> dx, dweight, dbias
+    balance_loss(logits, experts)               -> Balance (loss, counts, offsets, tokens)
+    balance_loss_backward(logits, balance, dloss) -> dlogits
 """
 from ._lib import (  # noqa: F401
     GA_BF16, GA_F16, GA_F32, GA_OK, GA_EINVAL, GA_EUNSUPPORTED, GA_EHIP, GA_MAX_D, GA_ROUND_INTERMEDIATES,
@@ -27,4 +38,11 @@ from ._lib import (  # noqa: F401
     DownPlan, GA_DOWN_MAX_ROWS, GA_DOWN_DECODE, GA_DOWN_STAGED, GA_DOWN_TILED,
     gelu_and_mul_sparse_down, plan_gelu_and_mul_sparse_down,
     gelu_and_mul_sparse_down_workspace_bytes, reserve_down_workspace,
+)
+from ._train import (  # noqa: F401
+    GA_ACT_SILU, GA_ACT_GELU_TANH, GA_ACT_GELU_ERF, GA_ACT_SQUARED_RELU, GA_ACT_GELU_SPARSE, ACTIVATIONS,
+    GA_CHECKPOINT_BLOCK, GA_LAYER_NORM_MAX_D, GA_BALANCE_MAX_EXPERTS, Checkpoint, Balance,
+    checkpoint_store, checkpoint_restore, activation_checkpoint, activation_backward,
+    layer_norm, layer_norm_checkpoint, layer_norm_backward, layer_norm_backward_workspace_bytes,
+    balance_loss, balance_loss_backward, balance_loss_workspace_bytes,
 )

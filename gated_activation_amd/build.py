@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libga.so")
 SOURCES = ["api.hip", "gelu_sparse.hip", "gelu_sparse_split.hip", "gelu_sparse_unaligned.hip", "gelu_sparse_rows.hip",
            "gelu_sparse_rep.hip", "gelu_sparse_decode.hip", "gelu_sparse_staged.hip", "gelu_sparse_tiled.hip",
-           "elementwise.hip"]
+           "elementwise.hip", "checkpoint.hip", "gelu_sparse_train.hip", "layer_norm.hip", "balance.hip", "train_api.hip"]
 ARCH = "gfx950"
 
 

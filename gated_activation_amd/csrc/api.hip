@@ -16,16 +16,18 @@
 #include <mutex>
 
 #include "../../include/ga.h"
+#include "ga_host.h"
 #include "ga_internal.h"
 
-namespace {
-
 // ---------------------------------------------------------------------------
-// Errors, sizes, pointer checks
+// What every entry point's file shares (ga_host.h)
 // ---------------------------------------------------------------------------
-thread_local char g_last_error[256] = "";
+namespace ga {
 
-ga_status fail(ga_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+static thread_local char g_last_error[256] = "";
+
+const char *last_error() { return g_last_error; }
+
 ga_status fail(ga_status st, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -48,6 +50,42 @@ bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
     return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
+// Compute-unit count of the current device, cached per device.
+static std::atomic<int> g_cus[64];
+
+ga_status current_cus(int *cus) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(GA_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
+    if (dev >= 0 && dev < 64) {
+        const int c = g_cus[dev].load(std::memory_order_relaxed);
+        if (c > 0) {
+            *cus = c;
+            return GA_OK;
+        }
+    }
+    int c = 0;
+    e = hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess || c <= 0)
+        return fail(GA_EHIP, "hipDeviceGetAttribute(CU count): %s", hipGetErrorString(e));
+    if (dev >= 0 && dev < 64) g_cus[dev].store(c, std::memory_order_relaxed);
+    *cus = c;
+    return GA_OK;
+}
+
+}  // namespace ga
+
+namespace {
+
+using ga::current_cus;
+using ga::elem_size;
+using ga::fail;
+using ga::launched;
+using ga::overlaps;
+
+// ---------------------------------------------------------------------------
+// Sizes, pointer checks
+// ---------------------------------------------------------------------------
 // The 16-byte path: both bases 16-byte aligned and every row a whole number
 // of 16-byte vectors.
 bool vector_aligned(const void *in, const void *out, int64_t d, int32_t dtype) {
@@ -78,29 +116,6 @@ ga_status check_rows(const char *op, const void *in, const void *out, int64_t ro
     const size_t out_bytes = (size_t)rows * (size_t)d * es;
     if (rows > 0 && overlaps(in, in_bytes, out, out_bytes))
         return fail(GA_EINVAL, "%s: in and out overlap (in-place is not supported)", op);
-    return GA_OK;
-}
-
-// Compute-unit count of the current device, cached per device.
-std::atomic<int> g_cus[64];
-
-ga_status current_cus(int *cus) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(GA_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
-    if (dev >= 0 && dev < 64) {
-        const int c = g_cus[dev].load(std::memory_order_relaxed);
-        if (c > 0) {
-            *cus = c;
-            return GA_OK;
-        }
-    }
-    int c = 0;
-    e = hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e != hipSuccess || c <= 0)
-        return fail(GA_EHIP, "hipDeviceGetAttribute(CU count): %s", hipGetErrorString(e));
-    if (dev >= 0 && dev < 64) g_cus[dev].store(c, std::memory_order_relaxed);
-    *cus = c;
     return GA_OK;
 }
 
@@ -1154,7 +1169,7 @@ const char *ga_status_str(int32_t status) {
     }
 }
 
-const char *ga_last_error(void) { return g_last_error; }
+const char *ga_last_error(void) { return ga::last_error(); }
 
 int32_t ga_version(void) { return 100; }
 

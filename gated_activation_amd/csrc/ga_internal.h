@@ -120,4 +120,60 @@ hipError_t launch_act(int op, int path, int dtype, int per_lane, int64_t grid, c
 hipError_t launch_xor_rows(int64_t grid, const void *in, void *out, int32_t rows,
                            uint32_t nvec_row, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Training kernels.  Codes are int8 [rows, halves * d], scales fp32
+// [rows, halves * ceil(d / 128)], stats fp32 [rows, 2]; any alignment natural
+// to the type.
+// ---------------------------------------------------------------------------
+// Elementwise: rows * halves * ceil(d / 128) < 2^31.  op: OP_* above, or -1 for
+// the plain store of an [rows, d] array (out unused).
+hipError_t launch_checkpoint_store(int dtype, int op, const void *in, void *out, void *codes, float *scales,
+                                   int32_t rows, uint32_t d, const int32_t *live, hipStream_t stream);
+hipError_t launch_checkpoint_restore(int dtype, const void *codes, const float *scales, const float *stats, void *out,
+                                     int32_t rows, uint32_t d, int32_t halves, const int32_t *live,
+                                     hipStream_t stream);
+// From in (x) where it is not null, else from codes and scales.
+hipError_t launch_act_backward(int dtype, int op, const void *dout, const void *in, const void *codes,
+                               const float *scales, void *dx, int32_t rows, uint32_t d, const int32_t *live,
+                               hipStream_t stream);
+
+// Sparse GELU, d <= 65536: one team of sparse_train_waves(d) wavefronts a row.
+int sparse_train_waves(int64_t d);
+hipError_t launch_sparse_store(int dtype, const void *in, void *out, void *codes, float *scales, float *stats,
+                               int32_t rows, int32_t d, float z, const int32_t *live, hipStream_t stream);
+hipError_t launch_sparse_backward(int dtype, const void *dout, const void *in, const void *codes, const float *scales,
+                                  const float *stats, void *dx, int32_t rows, int32_t d, float z, const int32_t *live,
+                                  hipStream_t stream);
+
+// Layer norm, d <= LN_MAX_D.  wide: weight, bias and their gradients are fp32,
+// else of `dtype`.  With codes, the forward also keeps fp32(x - mean) there.
+constexpr int64_t LN_MAX_D = 32768;
+hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
+                             void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
+                             const int32_t *live, hipStream_t stream);
+// Workgroups of the backward's first launch, each of which leaves one partial
+// row of the weight's and the bias' gradient in the workspace ([groups, 2, d]
+// fp32; unused when there is one group).  kept: from codes and scales, else
+// from in.
+int layer_norm_groups(int64_t rows, int64_t d, int cus);
+hipError_t launch_layer_norm_backward(int dtype, bool wide, const void *dout, const void *in, const void *codes,
+                                      const float *scales, const float *stats, const void *weight, void *dx,
+                                      void *dweight, void *dbias, bool kept, int32_t rows, int32_t d,
+                                      const int32_t *live, int groups, float *workspace, hipStream_t stream);
+
+// Balance loss, E <= BALANCE_MAX_E experts.  wide_index: int64 indices.
+constexpr int64_t BALANCE_MAX_E = 1024;
+int balance_groups(int64_t rows, int64_t experts, int cus);
+inline size_t balance_workspace_bytes(int groups, int64_t experts) {
+    return groups <= 1 ? 0 : (size_t)groups * (2 * (size_t)experts + 1) * 4;
+}
+hipError_t launch_balance(int dtype, const void *logits, const void *index, bool wide_index, const uint8_t *mask,
+                          float *loss, int32_t *counts, int32_t *offsets, int32_t *tokens, int32_t rows, int32_t experts,
+                          int32_t k, float coefficient, const int32_t *live, int groups, void *workspace,
+                          hipStream_t stream);
+hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t *mask, const int32_t *counts,
+                                   const int32_t *offsets, const int32_t *tokens, const float *dloss, void *dlogits,
+                                   int32_t rows, int32_t experts, int32_t k, float coefficient, const int32_t *live,
+                                   int cus, hipStream_t stream);
+
 }  // namespace ga

@@ -1,0 +1,357 @@
+// Device-side building blocks of the training kernels (gfx950, wave64): rows
+// moved in octets of eight consecutive elements, fp64 row statistics, the
+// 8-bit block code of activation checkpoints, and the activations with their
+// derivatives.
+#pragma once
+
+#include "ga_device.h"
+
+namespace ga {
+
+// ---------------------------------------------------------------------------
+// Octets: eight consecutive elements of a row per lane, so a 16-lane DPP row
+// holds one block of BLOCK8 = 128 values and a block's maximum needs no LDS.
+// The accesses are 16 bytes (two for fp32; 8 for codes) at the element's own
+// alignment: gfx950 runs global memory in unaligned-access mode, so one form
+// serves every alignment and only a row's last, partial octet (n < 8) goes
+// element by element.  Elements past the row read as zero.
+// ---------------------------------------------------------------------------
+constexpr int BLOCK8 = 128;
+
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+
+// An octet as loaded: the raw words, widened only when used.
+template <int DT> struct Oct {
+    static constexpr int WORDS = DT == DT_F32 ? 8 : 4;
+    uint32_t w[WORDS];
+};
+
+template <int DT>
+__device__ __forceinline__ void oct_zero(Oct<DT> &o) {
+#pragma unroll
+    for (int i = 0; i < Oct<DT>::WORDS; ++i) o.w[i] = 0;
+}
+
+template <int DT, bool NT = true>
+__device__ __forceinline__ void oct_load(Oct<DT> &o, const typename Elem<DT>::storage *p, int n) {
+    if (n >= 8) {
+        if constexpr (DT == DT_F32) {
+            const u32x4_a4 *q = reinterpret_cast<const u32x4_a4 *>(p);
+            u32x4 a, b;
+            if constexpr (NT) { a = __builtin_nontemporal_load(q); b = __builtin_nontemporal_load(q + 1); }
+            else { a = q[0]; b = q[1]; }
+            o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+            o.w[4] = b.x; o.w[5] = b.y; o.w[6] = b.z; o.w[7] = b.w;
+        } else {
+            const u32x4_a2 *q = reinterpret_cast<const u32x4_a2 *>(p);
+            u32x4 a;
+            if constexpr (NT) a = __builtin_nontemporal_load(q);
+            else a = *q;
+            o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+        }
+    } else {
+        oct_zero(o);
+#pragma unroll
+        for (int e = 0; e < 7; ++e) {
+            if (e < n) {
+                if constexpr (DT == DT_F32) o.w[e] = p[e];
+                else o.w[e >> 1] |= (uint32_t)p[e] << ((e & 1) * 16);
+            }
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void oct_unpack(const Oct<DT> &o, float (&f)[8]) {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, o.w[e]);
+    } else {
+        Elem<DT>::unpack(uint4{o.w[0], o.w[1], o.w[2], o.w[3]}, f);
+    }
+}
+
+// Rounds to the element type (ties to even) and stores the first n elements.
+template <int DT, bool NT = true>
+__device__ __forceinline__ void oct_store(typename Elem<DT>::storage *p, const float (&f)[8], int n) {
+    if constexpr (DT == DT_F32) {
+        if (n >= 8) {
+            u32x4_a4 *q = reinterpret_cast<u32x4_a4 *>(p);
+            const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+            const uint4 a = Elem<DT>::pack(lo), b = Elem<DT>::pack(hi);
+            const u32x4 va = {a.x, a.y, a.z, a.w}, vb = {b.x, b.y, b.z, b.w};
+            if constexpr (NT) { __builtin_nontemporal_store(va, q); __builtin_nontemporal_store(vb, q + 1); }
+            else { q[0] = va; q[1] = vb; }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < n) p[e] = Elem<DT>::from_f32(f[e]);
+        }
+    } else {
+        const uint4 a = Elem<DT>::pack(f);
+        if (n >= 8) {
+            u32x4_a2 *q = reinterpret_cast<u32x4_a2 *>(p);
+            const u32x4 va = {a.x, a.y, a.z, a.w};
+            if constexpr (NT) __builtin_nontemporal_store(va, q);
+            else *q = va;
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < n) p[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+        }
+    }
+}
+
+// Eight codes of a checkpoint (two words, element e in byte e).
+__device__ __forceinline__ uint2 codes_load(const uint8_t *p, int n) {
+    if (n >= 8) {
+        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1 *>(p));
+        return uint2{v.x, v.y};
+    }
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) w[e >> 2] |= (uint32_t)p[e] << ((e & 3) * 8);
+    return uint2{w[0], w[1]};
+}
+
+__device__ __forceinline__ void codes_store(uint8_t *p, uint2 c, int n) {
+    if (n >= 8) {
+        __builtin_nontemporal_store(u32x2{c.x, c.y}, reinterpret_cast<u32x2_a1 *>(p));
+        return;
+    }
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) p[e] = (uint8_t)(w[e >> 2] >> ((e & 3) * 8));
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit block code.  For a block of up to 128 values with largest
+// magnitude m (counted as at least 2^-100):
+//     code = round-half-even(127 x / m), the exact quotient,
+//     scale = fp32(m / 127), the value it stands for code * scale.
+// A block that holds a NaN, an infinity or a magnitude of 2^126 or more has
+// the scale NaN, so every value restored from it is NaN and shows.
+//
+// The quotient is formed in fp32 as y = x * (127 * rcp(m)), within 2^-22 of
+// itself (the reciprocal 2^-23, two roundings of 2^-24), 3.03e-5 at 127.  A
+// lane that has a y within 4e-5 of a half-integer forms that octet's
+// quotients again in fp64, where 127 x is exact and the quotient's distance
+// from a half-integer, if not zero, is at least 2^-26: far above fp64's error.
+// Adding 1.5 * 2^23 rounds y to an integer (ties to even) and leaves the code
+// in the low byte of the sum.
+// POSITIVE keeps the code of every x > 0 at 1 or more, so x > 0 can be read
+// back from the code exactly.
+// All 16 lanes of a DPP row hold octets of one block and call this together.
+// ---------------------------------------------------------------------------
+constexpr float ROUND_MAGIC = 12582912.0f;
+constexpr uint32_t LEAST_BITS = (127u - 100u) << 23;  // 2^-100
+constexpr uint32_t MOST_BITS = (127u + 126u) << 23;   // 2^126: below it the reciprocal is normal
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+    return v > o ? v : o;
+}
+
+template <bool POSITIVE>
+__device__ __forceinline__ uint2 block_encode(const float (&x)[8], float &scale) {
+    uint32_t top = LEAST_BITS;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu;  // orders NaN above infinity
+        top = top > a ? top : a;
+    }
+    top = dpp_umax<0xB1>(top);
+    top = dpp_umax<0x4E>(top);
+    top = dpp_umax<0x141>(top);
+    top = dpp_umax<0x140>(top);
+    const bool bad = top >= MOST_BITS;
+    const float m = __builtin_bit_cast(float, bad ? 0x3F800000u : top);
+    const float inv = 127.0f * __builtin_amdgcn_rcpf(m);
+    // fp32(m / 127): one correction step of the product with 1 / 127
+    const float s0 = m * (1.0f / 127.0f);
+    scale = __builtin_fmaf(__builtin_fmaf(-s0, 127.0f, m), 1.0f / 127.0f, s0);
+    float y[8], off = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        y[e] = __builtin_fmaf(x[e], inv, ROUND_MAGIC);
+        off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(x[e], inv, -(y[e] - ROUND_MAGIC))));
+    }
+    if (off > 0.49996f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = (float)__builtin_rint(127.0 * (double)x[e] / (double)m) + ROUND_MAGIC;
+    }
+    if constexpr (POSITIVE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (x[e] > 0.0f) y[e] = __builtin_fmaxf(y[e], ROUND_MAGIC + 1.0f);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t b0 = __builtin_bit_cast(uint32_t, y[4 * h]), b1 = __builtin_bit_cast(uint32_t, y[4 * h + 1]);
+        const uint32_t b2 = __builtin_bit_cast(uint32_t, y[4 * h + 2]), b3 = __builtin_bit_cast(uint32_t, y[4 * h + 3]);
+        // v_perm_b32 selects bytes of {src0, src1}: 0..3 from src1, 4..7 from src0
+        const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b3, b2, 0x04000C0Cu);
+        w[h] = bad ? 0u : (lo | hi);
+    }
+    if (bad) scale = __builtin_nanf("");
+    return uint2{w[0], w[1]};
+}
+
+// code * scale, rounded once: the byte with its sign bit flipped is code + 128,
+// and -128 * scale is exact.
+__device__ __forceinline__ void block_decode(uint2 c, float scale, float (&f)[8]) {
+    const float base = -128.0f * scale;
+    const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = __builtin_fmaf((float)((w[e >> 2] >> ((e & 3) * 8)) & 0xFFu), scale, base);
+}
+
+// ---------------------------------------------------------------------------
+// Row sums in fp64 (as fast as fp32 on this device outside packed math): lanes
+// paired as in wave_sum, so the result is the same on every lane.
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ double dpp_move64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double read_lane64(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double row16_sum(double v) {
+    v += dpp_move64<0xB1>(v);
+    v += dpp_move64<0x4E>(v);
+    v += dpp_move64<0x141>(v);
+    v += dpp_move64<0x140>(v);
+    return v;
+}
+
+__device__ __forceinline__ float row16_sum(float v) {
+    v += dpp_move<0xB1>(v);
+    v += dpp_move<0x4E>(v);
+    v += dpp_move<0x141>(v);
+    v += dpp_move<0x140>(v);
+    return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+    v = row16_sum(v);
+    return (read_lane64(v, 0) + read_lane64(v, 16)) + (read_lane64(v, 32) + read_lane64(v, 48));
+}
+
+// Sums of two values over the team that shares a row: 16 lanes, a wavefront,
+// or a workgroup of LANES / 64 wavefronts.  `slots`: LDS of 2 * LANES / 64
+// values that nothing else touches until the next barrier after this call.
+template <int LANES, typename T>
+__device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
+    if constexpr (LANES == 16) {
+        a = row16_sum(a);
+        b = row16_sum(b);
+    } else {
+        a = wave_sum(a);
+        b = wave_sum(b);
+        if constexpr (LANES > 64) {
+            constexpr int W = LANES / 64;
+            const int wave = threadIdx.x >> 6;
+            if ((threadIdx.x & 63) == 0) {
+                slots[2 * wave] = a;
+                slots[2 * wave + 1] = b;
+            }
+            __syncthreads();
+            a = slots[0];
+            b = slots[1];
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                a += slots[2 * i];
+                b += slots[2 * i + 1];
+            }
+        }
+    }
+}
+
+// Mean and population variance of d values from the sums of x - x0 and of its
+// square, x0 being the row's first value: one pass, one reduction, and a row
+// of one repeated value has variance 0 exactly.  In fp64 the differences of
+// fp32 values are exact or carry 2^-53, and the subtraction loses at most
+// (mean - x0)^2 / var <= d <= 2^16 times that.
+__device__ __forceinline__ void shifted_moments(double s1, double s2, double x0, double d, double &mean, double &var) {
+    const double m = s1 / d;
+    const double v = s2 / d - m * m;
+    mean = x0 + m;
+    var = v > 0.0 ? v : (v == v ? 0.0 : v);  // a NaN stays one
+}
+
+// ---------------------------------------------------------------------------
+// Activations with their derivatives, fp32.  ACT: the op codes of ga_internal.h.
+//   silu: p = 1 / (1 + e^-x); f = x p, f' = p + f (1 - p)
+//   gelu, tanh form: p = 1 / (1 + 2^(-x (A + B x^2))) (see gelu_tanh); f = x p,
+//     f' = p + f (1 - p) (1 + 3 * 0.044715 x^2) 2 sqrt(2 / pi)
+//   gelu, erf form: f = x Phi(x), f' = Phi(x) + x phi(x)
+//   squared relu: r = max(x, 0); f = r^2, f' = 2 r
+// For x << 0 p is 0 and f (1 - p) is x * 0; the power can overflow to +inf
+// (p = 0), never to NaN for finite x.
+// ---------------------------------------------------------------------------
+constexpr float GELU_DA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float GELU_DB = 0.21406444881780073f;  // 3 * 0.044715 * 2 sqrt(2 / pi)
+constexpr float INV_SQRT_2PI = 0.3989422804014327f;
+
+__device__ __forceinline__ void gelu_tanh_slope(float x, float &f, float &df) {
+    const float x2 = x * x;
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * __builtin_fmaf(GELU_B, x2, GELU_A)));
+    f = x * p;
+    const float q = f * (1.0f - p);
+    df = q == 0.0f ? p : __builtin_fmaf(q, __builtin_fmaf(GELU_DB, x2, GELU_DA), p);  // x^2 may be +inf there
+}
+
+__device__ __forceinline__ void silu_slope(float x, float &f, float &df) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * LOG2_E));
+    f = x * p;
+    df = __builtin_fmaf(f, 1.0f - p, p);
+}
+
+// Phi(x) = 0.5 erfc(-x / sqrt 2) with erfc_nonneg's rational approximation
+// (absolute error below 1.5e-7), whose e^(-x^2 / 2) also gives phi(x).
+__device__ __forceinline__ void gelu_erf_slope(float x, float &f, float &df) {
+    const float a = __builtin_fabsf(x) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, a, 1.0f));
+    const float e = __builtin_amdgcn_exp2f(-a * a * LOG2_E);
+    float poly = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+    poly = __builtin_fmaf(poly, t, 1.421413741f);
+    poly = __builtin_fmaf(poly, t, -0.284496736f);
+    poly = __builtin_fmaf(poly, t, 0.254829592f);
+    const float h = 0.5f * poly * t * e;
+    const float cdf = x < 0.0f ? h : 1.0f - h;
+    f = x * cdf;
+    df = __builtin_fmaf(x, INV_SQRT_2PI * e, cdf);
+}
+
+// Division of n < 2^31 by a fixed divisor: (mulhi(n, mul) + n) >> shift with
+// shift = ceil(log2 divisor), mul = floor(2^32 (2^shift - divisor) / divisor) + 1.
+struct FastDiv {
+    uint32_t mul, shift;
+    __host__ explicit FastDiv(uint32_t divisor) {
+        shift = 0;
+        while (((uint64_t)1 << shift) < divisor) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - divisor)) / divisor + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+}  // namespace ga

@@ -47,6 +47,7 @@
 #ifndef GA_H
 #define GA_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -310,6 +311,163 @@ ga_status ga_gelu_and_mul_sparse_down_with_plan(const void *gu, const void *w, v
                                                 int64_t H, int32_t dtype, float z, const int32_t *live_rows,
                                                 const ga_down_plan *plan, void *workspace,
                                                 size_t workspace_bytes, ga_stream stream);
+
+/*
+ * ---- Training ----
+ *
+ * The operators below are the training step around the gated activations.
+ * They follow the conventions above; any alignment natural to the element
+ * type is accepted, with the same kernels for all.  A written array overlaps
+ * no other array of the call (GA_EINVAL); an array without an element may be
+ * NULL.  live_rows bounds the rows as above (NULL: all); rows at or past it
+ * are neither read nor written.  Results do not depend on scheduling: every
+ * sum has a fixed order.
+ *
+ * Activation checkpoint: an array [rows, halves * d] kept in 8 bits for the
+ * backward pass.  Each row's halves (gate and up; one half for an ungated
+ * array) are cut into blocks of GA_CHECKPOINT_BLOCK = 128 values, the last one
+ * shorter.  With m the block's largest magnitude, counted as at least 2^-100:
+ *     code  = 127 x / m, the exact quotient rounded to the nearest integer
+ *             (ties to even), an int8 in [-127, 127]
+ *     scale = fp32(m / 127)
+ *     value = code * scale, within m / 254 of x (up to fp32 rounding)
+ * A block that holds a NaN, an infinity or a magnitude of 2^126 or more has
+ * the scale NaN: all values restored from it are NaN.
+ *   codes   int8 [rows, halves, d]
+ *   scales  fp32 [rows, halves, ceil(d / 128)]
+ *   stats   fp32 [rows, 2], where the codes are relative to their row:
+ *           (cutoff, std) for the sparse GELU, whose first half holds
+ *           fp32(gate - cutoff); (mean, 1 / std) for layer norm, which holds
+ *           fp32(x - mean).
+ */
+#define GA_CHECKPOINT_BLOCK 128
+
+/* x [rows, d] -> codes, scales (one half).  1 <= d <= GA_MAX_D; rows *
+ * ceil(d / 128) < 2^31 (else GA_EUNSUPPORTED). */
+ga_status ga_checkpoint_store(const void *in, void *codes, float *scales, int64_t rows, int64_t d, int32_t dtype,
+                              const int32_t *live_rows, ga_stream stream);
+
+/* codes, scales -> out [rows, halves * d] of `dtype`: code * scale, plus
+ * stats[row][0] in the first half where stats is given, in fp32, rounded once
+ * to the type. */
+ga_status ga_checkpoint_restore(const void *codes, const float *scales, const float *stats, void *out, int64_t rows,
+                                int64_t d, int32_t halves, int32_t dtype, const int32_t *live_rows, ga_stream stream);
+
+/*
+ * The activations of the training pair.  f(gate) * up of in [rows, 2d] for
+ * SILU, GELU_TANH, GELU_ERF; max(in, 0)^2 of in [rows, d] for SQUARED_RELU;
+ * GELU_SPARSE as ga_gelu_and_mul_sparse with cutoff multiplier z (z is not
+ * looked at otherwise).
+ */
+typedef enum {
+    GA_ACT_SILU = 0,
+    GA_ACT_GELU_TANH = 1,
+    GA_ACT_GELU_ERF = 2,
+    GA_ACT_SQUARED_RELU = 3,
+    GA_ACT_GELU_SPARSE = 4
+} ga_activation;
+
+/*
+ * The activation's forward pass that keeps its input: one pass over in,
+ * writing out [rows, d] (the value of the forward-only entry points, up to
+ * fp32 rounding) and codes and scales of in (two halves; one for
+ * SQUARED_RELU).  GELU_SPARSE: t = fp32(gate - cutoff) is kept in place of the
+ * gate, with codes of at least 1 where t > 0, so the backward pass masks
+ * exactly the values that the forward pass did; cutoff and std (statistics in
+ * fp64) go to stats, which the others do not use (NULL).
+ */
+ga_status ga_activation_checkpoint(const void *in, void *out, void *codes, float *scales, float *stats, int64_t rows,
+                                   int64_t d, int32_t dtype, int32_t activation, float z, const int32_t *live_rows,
+                                   ga_stream stream);
+
+/*
+ * The gradient dx (in's shape) from dout [rows, d], in fp32, rounded once:
+ *     dgate = dout up f'(gate), dup = dout f(gate); squared ReLU 2 max(in, 0) dout
+ * GELU_SPARSE, with mean m and std s of the row's gate, t = gate - m - z s,
+ * q = dout up gelu'(t) where t > 0 and 0 elsewhere, G the row's sum of q:
+ *     dgate = q - (G / d) (1 + z (gate - m) / s), dup = dout gelu(max(t, 0))
+ * the gradient through the row's mean and std too; the term with s is 0 where
+ * s is 0, as the derivative of a std that is 0 is taken to be.  Statistics and
+ * the side of the cutoff are fp64.
+ * _checkpoint: the same formulas at the values that codes, scales (and stats)
+ * stand for.
+ */
+ga_status ga_activation_backward(const void *dout, const void *in, void *dx, int64_t rows, int64_t d, int32_t dtype,
+                                 int32_t activation, float z, const int32_t *live_rows, ga_stream stream);
+ga_status ga_activation_backward_checkpoint(const void *dout, const void *codes, const float *scales,
+                                            const float *stats, void *dx, int64_t rows, int64_t d, int32_t dtype,
+                                            int32_t activation, float z, const int32_t *live_rows, ga_stream stream);
+
+/*
+ * Layer norm of in [rows, d]: with the row's mean m and population variance v,
+ *     r = 1 / sqrt(v + eps), out = (in - m) r weight + bias
+ * stats [rows, 2] = (m, r).  weight and bias (NULL: none) [d] are of
+ * weight_dtype, which is dtype or GA_F32.  d <= GA_LAYER_NORM_MAX_D; eps >= 0.
+ * _checkpoint also keeps fp32(in - m) in codes and scales (one half).
+ */
+#define GA_LAYER_NORM_MAX_D 32768
+ga_status ga_layer_norm(const void *in, const void *weight, const void *bias, void *out, float *stats, int64_t rows,
+                        int64_t d, int32_t dtype, int32_t weight_dtype, float eps, const int32_t *live_rows,
+                        ga_stream stream);
+ga_status ga_layer_norm_checkpoint(const void *in, const void *weight, const void *bias, void *out, void *codes,
+                                   float *scales, float *stats, int64_t rows, int64_t d, int32_t dtype,
+                                   int32_t weight_dtype, float eps, const int32_t *live_rows, ga_stream stream);
+
+/*
+ * Layer norm's backward pass from dout [rows, d]: with n = (in - m) r (or r
+ * times the value a code stands for) and v = dout weight,
+ *     dx = r (v - mean(v) - n mean(v n)) per row
+ *     dweight = sum over live rows of dout n, dbias = sum of dout (NULL: not wanted)
+ * dx of dtype, dweight and dbias of weight_dtype, sums in fp32.  No live rows:
+ * dweight and dbias are zero.
+ *   workspace  ga_layer_norm_backward_workspace_bytes(rows, d) bytes, 16-byte
+ *              aligned, any content; calls that share one must not overlap in
+ *              time.
+ */
+size_t ga_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+ga_status ga_layer_norm_backward(const void *dout, const void *in, const float *stats, const void *weight, void *dx,
+                                 void *dweight, void *dbias, int64_t rows, int64_t d, int32_t dtype,
+                                 int32_t weight_dtype, const int32_t *live_rows, void *workspace,
+                                 size_t workspace_bytes, ga_stream stream);
+ga_status ga_layer_norm_backward_checkpoint(const void *dout, const void *codes, const float *scales,
+                                            const float *stats, const void *weight, void *dx, void *dweight,
+                                            void *dbias, int64_t rows, int64_t d, int32_t dtype, int32_t weight_dtype,
+                                            const int32_t *live_rows, void *workspace, size_t workspace_bytes,
+                                            ga_stream stream);
+
+/*
+ * The router's balance loss over the n tokens (rows) that count: below the
+ * live count and, where mask is given, with a mask byte other than 0.
+ *     p = softmax(logits) over the experts, in fp32
+ *     counts[e] = number of chosen indices equal to e (int32 [experts])
+ *     loss = coefficient * experts / (k n) * sum over e of counts[e] P[e],
+ *            P[e] = (sum over tokens of p[t, e]) / n
+ * (coefficient when tokens and probabilities are spread evenly; 0 for n = 0).
+ *   logits   [rows, experts] of dtype, 1 <= experts <= GA_BALANCE_MAX_EXPERTS
+ *   index    [rows, k] int32 or int64 (index_bytes 4 or 8): the experts of each
+ *            token; values outside [0, experts) (a dropped choice) are not
+ *            counted.  rows * k < 2^31.
+ *   offsets  int32 [experts + 1], the running sum of counts: expert e's first
+ *            row in a buffer sorted by expert, and in offsets[experts] the
+ *            buffer's live rows, which the bounded activations read as
+ *            live_rows.
+ *   tokens   int32: n.
+ * A token whose logits are all -infinity has p = 0.
+ * Backward, with counts as constants and dloss a device fp32:
+ *     dlogits = dloss coefficient experts / (k n^2) p (counts - sum_j counts[j] p[j])
+ * rows of tokens that do not count get 0 (past the live count: untouched).
+ *   workspace  as for layer norm, ga_balance_loss_workspace_bytes() bytes.
+ */
+#define GA_BALANCE_MAX_EXPERTS 1024
+size_t ga_balance_loss_workspace_bytes(int64_t rows, int64_t experts);
+ga_status ga_balance_loss(const void *logits, const void *index, int32_t index_bytes, const uint8_t *mask, float *loss,
+                          int32_t *counts, int32_t *offsets, int32_t *tokens, int64_t rows, int64_t experts, int64_t k,
+                          int32_t dtype, float coefficient, const int32_t *live_rows, void *workspace,
+                          size_t workspace_bytes, ga_stream stream);
+ga_status ga_balance_loss_backward(const void *logits, const uint8_t *mask, const int32_t *counts,
+                                   const int32_t *offsets, const int32_t *tokens, const float *dloss, void *dlogits,
+                                   int64_t rows, int64_t experts, int64_t k, int32_t dtype, float coefficient,
+                                   const int32_t *live_rows, ga_stream stream);
 
 /*
  * Host-only helper: z = Phi^-1(target_sparsity), the cutoff multiplier for
