@@ -45,9 +45,10 @@ __device__ __forceinline__ void act_slope(float x, float &f, float &df) {
 }
 
 // One half's block: codes and, from the block's first lane, its scale.
+template <int DT>
 __device__ __forceinline__ void keep_block(const float (&x)[8], uint8_t *codes, float *scale_at, int n, bool first) {
     float scale;
-    const uint2 c = block_encode<false>(x, scale);
+    const uint2 c = block_encode<code_of<DT>(), false>(x, scale);
     codes_store(codes, c, n);
     if (first) *scale_at = scale;
 }
@@ -88,14 +89,14 @@ __global__ __launch_bounds__(FLAT_BLOCK) void store_kernel(
             oct_unpack<DT>(g[k], x);
             const size_t at = (size_t)row[k] * (H * d) + col[k];
             const size_t block = (size_t)row[k] * (H * nb) + (b - row[k] * nb);
-            keep_block(x, codes + at, scales + block, n[k], l8 == 0);
+            keep_block<DT>(x, codes + at, scales + block, n[k], l8 == 0);
             if constexpr (ACT >= 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = act_value<ACT>(x[e]);
                 if constexpr (GATED) {
                     float up[8];
                     oct_unpack<DT>(u[k], up);
-                    keep_block(up, codes + at + d, scales + block + nb, n[k], l8 == 0);
+                    keep_block<DT>(up, codes + at + d, scales + block + nb, n[k], l8 == 0);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] *= up[e];
                 }

@@ -150,7 +150,7 @@ hipError_t launch_sparse_backward(int dtype, const void *dout, const void *in, c
 constexpr int64_t LN_MAX_D = 32768;
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
                              void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
-                             const int32_t *live, hipStream_t stream);
+                             const int32_t *live, int cus, hipStream_t stream);
 // Workgroups of the backward's first launch, each of which leaves one partial
 // row of the weight's and the bias' gradient in the workspace ([groups, 2, d]
 // fp32; unused when there is one group).  kept: from codes and scales, else

@@ -133,17 +133,33 @@ __device__ __forceinline__ void codes_store(uint8_t *p, uint2 c, int n) {
 // The 8-bit block code.  For a block of up to 128 values with largest
 // magnitude m (counted as at least 2^-100):
 //     code = round-half-even(127 x / m), the exact quotient,
-//     scale = fp32(m / 127), the value it stands for code * scale.
+//     scale = m / 127 in fp32 (within 2^-23), the value it stands for code * scale.
 // A block that holds a NaN, an infinity or a magnitude of 2^126 or more has
 // the scale NaN, so every value restored from it is NaN and shows.
 //
-// The quotient is formed in fp32 as y = x * (127 * rcp(m)), within 2^-22 of
-// itself (the reciprocal 2^-23, two roundings of 2^-24), 3.03e-5 at 127.  A
-// lane that has a y within 4e-5 of a half-integer forms that octet's
-// quotients again in fp64, where 127 x is exact and the quotient's distance
-// from a half-integer, if not zero, is at least 2^-26: far above fp64's error.
-// Adding 1.5 * 2^23 rounds y to an integer (ties to even) and leaves the code
-// in the low byte of the sum.
+// The quotient is formed in fp32 as y = x inv, inv = 127 rcp(m).  Adding
+// 1.5 * 2^23 rounds y to an integer (ties to even) and leaves the code in the
+// low byte of the sum.  That is the exact quotient's rounding unless a
+// half-integer h / 2 (h odd) lies on the quotient or between it and y:
+//   x and m of 11 significant bits or fewer (fp16 and bf16 inputs), as
+//   u 2^-j and M in units of m's last bit: 127 x / m = h / 2 or
+//   |127 x / m - h / 2| = |254 u 2^-j - h M| / (2 M) >= 2^-j / 4094.  inv is
+//   raised by 3 * 2^-23 here, so it lies above 127 / m, by at most 5 * 2^-23 of
+//   it (the reciprocal is within 2^-23, two products round by 2^-24 each), and
+//   y is off by less than 254 * 6e-7 * 2^-j.  So only ties matter: h M =
+//   254 u 2^-j needs 127 to divide h M.  h = +-127 is x = +-m / 2, whose y above
+//   63.5 rounds to 64, as ties to even do; otherwise 127 divides M (one block
+//   in about 128), and that block's quotients are formed in fp64.
+//   any fp32 x: y is within 2^-22 of itself, 3.03e-5 at 127.  A lane that has a
+//   y within 4e-5 of a half-integer forms its quotients again in fp64, where
+//   127 x is exact and the quotient's distance from a half-integer, if not
+//   zero, is at least 2^-26.
+//   fp32 differences of 16-bit rows from their mean or cutoff: y as it is, so a
+//   quotient within 3.03e-5 of a half-integer may go to either side (the check
+//   is 2.5 instructions a value of about 40).
+// (Checking every y of 16-bit inputs too took the fp64 path in most
+// wavefronts, since a bf16 block often holds half its largest value: the silu
+// forward at 12288 rows of 768 then took 18.2 us, 14.1 us without.)
 // POSITIVE keeps the code of every x > 0 at 1 or more, so x > 0 can be read
 // back from the code exactly.
 // All 16 lanes of a DPP row hold octets of one block and call this together.
@@ -158,34 +174,59 @@ __device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
     return v > o ? v : o;
 }
 
-template <bool POSITIVE>
-__device__ __forceinline__ uint2 block_encode(const float (&x)[8], float &scale) {
-    uint32_t top = LEAST_BITS;
+// Which of the three an octet's values are.
+enum CodeOf { OF_F16, OF_BF16, OF_F32, OF_DIFFERENCE };
+template <int DT> constexpr CodeOf code_of() { return DT == DT_F32 ? OF_F32 : DT == DT_F16 ? OF_F16 : OF_BF16; }
+template <int DT> constexpr CodeOf difference_of() { return DT == DT_F32 ? OF_F32 : OF_DIFFERENCE; }
+
+// What encodes a block: 127 / m, the scale, and m itself.
+struct Block8 {
+    float inv, scale, m;
+    bool bad, check;
+};
+
+template <CodeOf OF>
+__device__ __forceinline__ Block8 block_scale(const float (&x)[8]) {
+    // the IEEE maximum, which a NaN wins
+    float a = __builtin_fabsf(x[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t a = __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu;  // orders NaN above infinity
-        top = top > a ? top : a;
-    }
+    for (int e = 1; e < 8; ++e) a = __builtin_elementwise_maximum(a, __builtin_fabsf(x[e]));
+    // as integers: NaN above infinity above every number
+    uint32_t top = __builtin_bit_cast(uint32_t, a) & 0x7FFFFFFFu;
     top = dpp_umax<0xB1>(top);
     top = dpp_umax<0x4E>(top);
     top = dpp_umax<0x141>(top);
     top = dpp_umax<0x140>(top);
-    const bool bad = top >= MOST_BITS;
-    const float m = __builtin_bit_cast(float, bad ? 0x3F800000u : top);
-    const float inv = 127.0f * __builtin_amdgcn_rcpf(m);
-    // fp32(m / 127): one correction step of the product with 1 / 127
-    const float s0 = m * (1.0f / 127.0f);
-    scale = __builtin_fmaf(__builtin_fmaf(-s0, 127.0f, m), 1.0f / 127.0f, s0);
-    float y[8], off = 0.0f;
+    Block8 b;
+    b.bad = top >= MOST_BITS;
+    top = top > LEAST_BITS ? top : LEAST_BITS;
+    b.m = __builtin_bit_cast(float, b.bad ? 0x3F800000u : top);
+    b.inv = 127.0f * __builtin_amdgcn_rcpf(b.m);
+    if constexpr (OF == OF_F16 || OF == OF_BF16) b.inv *= 1.0f + 0x3p-23f;
+    b.scale = b.bad ? __builtin_nanf("") : b.m * (1.0f / 127.0f);
+    // does 127 divide m's significand?
+    if constexpr (OF == OF_F16) b.check = (1024u + ((top >> 13) & 0x3FFu)) % 127u == 0u;
+    else b.check = OF == OF_BF16 && (top & 0x7F0000u) == 0x7E0000u;
+    return b;
+}
+
+template <CodeOf OF, bool POSITIVE>
+__device__ __forceinline__ uint2 block_codes(const Block8 &b, const float (&x)[8]) {
+    float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        y[e] = __builtin_fmaf(x[e], inv, ROUND_MAGIC);
-        off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(x[e], inv, -(y[e] - ROUND_MAGIC))));
-    }
-    if (off > 0.49996f) {
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(x[e], b.inv, ROUND_MAGIC);
+    bool again = b.check;
+    if constexpr (OF == OF_F32) {
+        float off = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            y[e] = (float)__builtin_rint(127.0 * (double)x[e] / (double)m) + ROUND_MAGIC;
+            off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(x[e], b.inv, -(y[e] - ROUND_MAGIC))));
+        again = off > 0.49996f;
+    }
+    if (OF != OF_DIFFERENCE && again) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = (float)__builtin_rint(127.0 * (double)x[e] / (double)b.m) + ROUND_MAGIC;
     }
     if constexpr (POSITIVE) {
 #pragma unroll
@@ -199,11 +240,17 @@ __device__ __forceinline__ uint2 block_encode(const float (&x)[8], float &scale)
         const uint32_t b2 = __builtin_bit_cast(uint32_t, y[4 * h + 2]), b3 = __builtin_bit_cast(uint32_t, y[4 * h + 3]);
         // v_perm_b32 selects bytes of {src0, src1}: 0..3 from src1, 4..7 from src0
         const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x0C0C0400u);
-        const uint32_t hi = __builtin_amdgcn_perm(b3, b2, 0x04000C0Cu);
-        w[h] = bad ? 0u : (lo | hi);
+        const uint32_t hi = __builtin_amdgcn_perm(b3, b2, 0x0C0C0400u);
+        w[h] = b.bad ? 0u : __builtin_amdgcn_perm(hi, lo, 0x05040100u);
     }
-    if (bad) scale = __builtin_nanf("");
     return uint2{w[0], w[1]};
+}
+
+template <CodeOf OF, bool POSITIVE>
+__device__ __forceinline__ uint2 block_encode(const float (&x)[8], float &scale) {
+    const Block8 b = block_scale<OF>(x);
+    scale = b.scale;
+    return block_codes<OF, POSITIVE>(b, x);
 }
 
 // code * scale, rounded once: the byte with its sign bit flipped is code + 128,
@@ -223,8 +270,8 @@ __device__ __forceinline__ void block_decode(uint2 c, float scale, float (&f)[8]
 template <int CTRL>
 __device__ __forceinline__ double dpp_move64(double v) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
@@ -257,8 +304,9 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // Sums of two values over the team that shares a row: 16 lanes, a wavefront,
-// or a workgroup of LANES / 64 wavefronts.  `slots`: LDS of 2 * LANES / 64
-// values that nothing else touches until the next barrier after this call.
+// or LANES / 64 wavefronts of a workgroup (all of whose teams call it together).
+// `slots`: LDS of the team's own, 2 * LANES / 64 values that nothing else
+// touches until the next barrier after this call.
 template <int LANES, typename T>
 __device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
     if constexpr (LANES == 16) {
@@ -269,7 +317,7 @@ __device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
         b = wave_sum(b);
         if constexpr (LANES > 64) {
             constexpr int W = LANES / 64;
-            const int wave = threadIdx.x >> 6;
+            const int wave = (threadIdx.x % LANES) >> 6;
             if ((threadIdx.x & 63) == 0) {
                 slots[2 * wave] = a;
                 slots[2 * wave + 1] = b;
@@ -285,6 +333,43 @@ __device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
         }
     }
 }
+
+// Adds an octet's x - x0 and (x - x0)^2 to fp64 sums.  Differences of 16-bit
+// values are exact in fp32 up to 2^-24 of x0, and so are their sums of eight,
+// far below what decides a rounding of the row's result; squares go to fp64.
+template <int DT>
+__device__ __forceinline__ void add_shifted(const float (&x)[8], float x0, double &s1, double &s2) {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double a = (double)x[e] - (double)x0;
+            s1 += a;
+            s2 = __builtin_fma(a, a, s2);
+        }
+    } else {
+        float a[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = x[e] - x0;
+            const double b = a[e];
+            s2 = __builtin_fma(b, b, s2);
+        }
+        s1 += (double)(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
+    }
+}
+
+// x - at, at an fp64 value of the row.  16-bit rows take at as the sum of two
+// fp32 numbers: x - hi is exact where x is near hi, so the difference's sign
+// is exact and its value within two roundings; fp32 rows round it once.
+template <int DT> struct RowOrigin {
+    float hi, lo;
+    double at;
+    __device__ __forceinline__ explicit RowOrigin(double v) : hi((float)v), lo((float)(v - (double)(float)v)), at(v) {}
+    __device__ __forceinline__ float from(float x) const {
+        if constexpr (DT == DT_F32) return (float)((double)x - at);
+        else return (x - hi) - lo;
+    }
+};
 
 // Mean and population variance of d values from the sums of x - x0 and of its
 // square, x0 being the row's first value: one pass, one reduction, and a row

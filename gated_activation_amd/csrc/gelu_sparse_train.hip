@@ -45,7 +45,6 @@ __device__ __forceinline__ RowAt row_of_team() {
 template <int DT, int W, int V>
 __device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lane, int d, float first, double *slots,
                                              double &mean, double &var) {
-    const double x0 = first;
     double s1 = 0.0, s2 = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -56,31 +55,30 @@ __device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lan
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] : first;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double a = (double)x[e] - x0;
-            s1 += a;
-            s2 = __builtin_fma(a, a, s2);
-        }
+        add_shifted<DT>(x, first, s1, s2);
     }
     team_sum2<64 * W>(s1, s2, slots);
-    shifted_moments(s1, s2, x0, (double)d, mean, var);
+    shifted_moments(s1, s2, (double)first, (double)d, mean, var);
 }
 
 // fp32(gate - cutoff) of an octet; 0 past the row's end.
 template <int DT>
-__device__ __forceinline__ void over_cutoff(const Oct<DT> &g, double cutoff, int n, float (&t)[8]) {
+__device__ __forceinline__ void over_cutoff(const Oct<DT> &g, const RowOrigin<DT> &cutoff, int n, float (&t)[8]) {
     oct_unpack<DT>(g, t);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = (float)((double)t[e] - cutoff);
+    for (int e = 0; e < 8; ++e) t[e] = cutoff.from(t[e]);
     if (n < 8) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = e < n ? t[e] : 0.0f;
     }
 }
 
+// Waves a SIMD holds at least: 16-wave workgroups of two octets a lane pair up
+// on a compute unit within 64 registers (a third register pair halves that).
+template <int DT, int W, int V> constexpr int sparse_waves() { return DT != DT_F32 && W == 16 && V == 2 ? 8 : 4; }
+
 template <int DT, int W, int V>
-__global__ __launch_bounds__(team_block<W>()) void sparse_store_kernel(
+__global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void sparse_store_kernel(
     const typename Elem<DT>::storage *__restrict__ in, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
     uint32_t nb, float z, const int32_t *__restrict__ live) {
@@ -95,13 +93,19 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_store_kernel(
         const int c = (int)(v * 64 * W + at.lane) * 8;
         oct_load<DT>(g[v], x + c, d - c);
     }
+    Oct<DT> u[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (int)(v * 64 * W + at.lane) * 8;
+        oct_load<DT>(u[v], x + d + c, d - c);
+    }
     const float first = Elem<DT>::to_f32(x[0]);
     double mean, var;
     gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
     const double std = __builtin_sqrt(var);
-    const double cutoff = __builtin_fma((double)z, std, mean);
+    const RowOrigin<DT> cutoff(__builtin_fma((double)z, std, mean));
     if (at.lane == 0) {
-        stats[2 * (size_t)at.row] = (float)cutoff;
+        stats[2 * (size_t)at.row] = cutoff.hi;
         stats[2 * (size_t)at.row + 1] = (float)std;
     }
     uint8_t *row_codes = codes + (size_t)at.row * 2 * d;
@@ -112,15 +116,13 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_store_kernel(
         const int n = d - c;
         const uint32_t block = (uint32_t)c / BLOCK8;
         if (block >= nb) continue;  // the same for the 16 lanes of a block
-        Oct<DT> u;
-        oct_load<DT>(u, x + d + c, n);
         float t[8], up[8], scale;
         over_cutoff<DT>(g[v], cutoff, n, t);
-        const uint2 ct = block_encode<true>(t, scale);
+        const uint2 ct = block_encode<difference_of<DT>(), true>(t, scale);
         codes_store(row_codes + c, ct, n);
         if ((at.lane & 15) == 0) row_scales[block] = scale;
-        oct_unpack<DT>(u, up);
-        const uint2 cu = block_encode<false>(up, scale);
+        oct_unpack<DT>(u[v], up);
+        const uint2 cu = block_encode<code_of<DT>(), false>(up, scale);
         codes_store(row_codes + d + c, cu, n);
         if ((at.lane & 15) == 0) row_scales[nb + block] = scale;
 #pragma unroll
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
     Oct<DT> g[KEPT ? 1 : V];
     uint2 ct[KEPT ? V : 1];
     float st[KEPT ? V : 1];
-    double cutoff = 0.0;
+    RowOrigin<DT> cutoff(0.0);
     float s;
     if constexpr (KEPT) {
         s = stats[2 * (size_t)at.row + 1];
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
         double mean, var;
         gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
         const double std = __builtin_sqrt(var);
-        cutoff = __builtin_fma((double)z, std, mean);
+        cutoff = RowOrigin<DT>(__builtin_fma((double)z, std, mean));
         s = (float)std;
     }
     float q[V][8], total = 0.0f;

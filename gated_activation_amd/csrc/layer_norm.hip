@@ -28,33 +28,47 @@ namespace ga {
 
 namespace {
 
-template <int LANES> constexpr int ln_block() { return LANES < 256 && LANES <= 64 ? 256 : LANES; }
-
 // fp32 weights where WIDE, else the rows' type.
 template <int DT, bool WIDE> constexpr int weight_type() { return WIDE ? DT_F32 : DT; }
 
+// The team of a row by its width: LANES lanes of V octets.  Two octets a lane
+// halve what the row's reductions cost a value; a row of up to 1024 values is
+// a wavefront's own and needs no barrier.
+template <int LANES_, int V_> struct Team {
+    static constexpr int LANES = LANES_, V = V_;
+};
+
+template <typename F>
+auto by_width(int64_t d, F &&f) {
+    if (d <= 128) return f(Team<16, 1>());
+    if (d <= 512) return f(Team<64, 1>());
+    if (d <= 1024) return f(Team<64, 2>());
+    if (d <= 2048) return f(Team<128, 2>());
+    if (d <= 4096) return f(Team<256, 2>());
+    if (d <= 8192) return f(Team<512, 2>());
+    if (d <= 16384) return f(Team<1024, 2>());
+    return f(Team<1024, 4>());
+}
+
+constexpr int FORWARD_BLOCK = 256;  // workgroups of several teams; a larger team is one by itself
+template <int LANES> constexpr int forward_block() { return LANES > FORWARD_BLOCK ? LANES : FORWARD_BLOCK; }
+
+// One row of a team, and the rows its workgroup's teams take in turn.
 template <int DT, bool WIDE, int LANES, int V, bool KEEP>
-__global__ __launch_bounds__(ln_block<LANES>()) void forward_kernel(
+__global__ __launch_bounds__(forward_block<LANES>(), 4) void forward_kernel(
     const typename Elem<DT>::storage *__restrict__ in,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ bias, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
     float eps, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
-    constexpr int TEAMS = ln_block<LANES>() / LANES;
-    __shared__ double slots[LANES > 64 ? LANES / 32 : 1];
-    const uint32_t lane = threadIdx.x % LANES;
-    const uint32_t row = blockIdx.x * TEAMS + threadIdx.x / LANES;
+    constexpr int TEAMS = forward_block<LANES>() / LANES, WAVES = LANES > 64 ? LANES / 64 : 1;
+    __shared__ double slots[2][TEAMS][2 * WAVES];
+    const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
-    if (row >= live_rows) return;
-    const typename Elem<DT>::storage *x = in + (size_t)row * d;
-    Oct<DT> o[V];
+    const uint32_t step = gridDim.x * TEAMS;
+    const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
     Oct<WT> w[V], b[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * LANES + lane) * 8;
-        oct_load<DT>(o[v], x + c, d - c);
-    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * LANES + lane) * 8;
@@ -62,69 +76,92 @@ __global__ __launch_bounds__(ln_block<LANES>()) void forward_kernel(
         if (bias != nullptr) oct_load<WT, false>(b[v], bias + c, d - c);
         else oct_zero(b[v]);
     }
-    const float first = Elem<DT>::to_f32(x[0]);
-    const double x0 = first;
-    double s1 = 0.0, s2 = 0.0;
+    Oct<DT> next[V];
+    float next_first = 0.0f;
+    auto load = [&](uint32_t row) {
+        if (row >= live_rows) return;
+        const typename Elem<DT>::storage *x = in + (size_t)row * d;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int n = d - (int)(v * LANES + lane) * 8;
-        float f[8];
-        oct_unpack<DT>(o[v], f);
-        if (n < 8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : first;
+        for (int v = 0; v < V; ++v) {
+            const int c = (int)(v * LANES + lane) * 8;
+            oct_load<DT>(next[v], x + c, d - c);
         }
+        next_first = Elem<DT>::to_f32(x[0]);
+    };
+    load(blockIdx.x * TEAMS + team);
+    int turn = 0;
+    for (uint32_t base = blockIdx.x * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
+        const uint32_t row = base + team;
+        Oct<DT> o[V];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double a = (double)f[e] - x0;
-            s1 += a;
-            s2 = __builtin_fma(a, a, s2);
-        }
-    }
-    team_sum2<LANES>(s1, s2, slots);
-    double mean, var;
-    shifted_moments(s1, s2, x0, (double)d, mean, var);
-    const float rstd = (float)(1.0 / __builtin_sqrt(var + (double)eps));
-    if (lane == 0) {
-        stats[2 * (size_t)row] = (float)mean;
-        stats[2 * (size_t)row + 1] = rstd;
-    }
-    const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
+        for (int v = 0; v < V; ++v) o[v] = next[v];
+        const float first = next_first;
+        load(row + step);
+        double s1 = 0.0, s2 = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * LANES + lane) * 8;
-        const int n = d - c;
-        const uint32_t block = (uint32_t)c / BLOCK8;
-        if (block >= nb) continue;  // the same for the 16 lanes of a block
-        float f[8], wf[8], bf[8];
-        oct_unpack<DT>(o[v], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (float)((double)f[e] - mean);
-        if constexpr (KEEP) {
+        for (int v = 0; v < V; ++v) {
+            const int n = d - (int)(v * LANES + lane) * 8;
+            float f[8];
+            oct_unpack<DT>(o[v], f);
             if (n < 8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : 0.0f;
+                for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : first;
             }
-            float scale;
-            const uint2 k = block_encode<false>(f, scale);
-            codes_store(codes + (size_t)row * d + c, k, n);
-            if ((lane & 15) == 0) scales[(size_t)row * nb + block] = scale;
+            add_shifted<DT>(f, first, s1, s2);
         }
-        oct_unpack<WT>(w[v], wf);
-        oct_unpack<WT>(b[v], bf);
+        team_sum2<LANES>(s1, s2, slots[turn][team]);
+        turn ^= 1;
+        if (row >= live_rows) continue;
+        double m, var;
+        shifted_moments(s1, s2, (double)first, (double)d, m, var);
+        const RowOrigin<DT> mean(m);
+        const float rstd = (float)(1.0 / __builtin_sqrt(var + (double)eps));
+        if (lane == 0) {
+            stats[2 * (size_t)row] = mean.hi;
+            stats[2 * (size_t)row + 1] = rstd;
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, wf[e], bf[e]);
-        oct_store<DT>(out + (size_t)row * d + c, f, n);
+        for (int v = 0; v < V; ++v) {
+            const int c = (int)(v * LANES + lane) * 8;
+            const int n = d - c;
+            const uint32_t block = (uint32_t)c / BLOCK8;
+            if (block >= nb) continue;  // the same for the 16 lanes of a block
+            float f[8], wf[8], bf[8];
+            oct_unpack<DT>(o[v], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = mean.from(f[e]);
+            if constexpr (KEEP) {
+                if (n < 8) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : 0.0f;
+                }
+                float scale;
+                const uint2 k = block_encode<difference_of<DT>(), false>(f, scale);
+                codes_store(codes + (size_t)row * d + c, k, n);
+                if ((lane & 15) == 0) scales[(size_t)row * nb + block] = scale;
+            }
+            oct_unpack<WT>(w[v], wf);
+            oct_unpack<WT>(b[v], bf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, wf[e], bf[e]);
+            oct_store<DT>(out + (size_t)row * d + c, f, n);
+        }
     }
 }
 
-// Waves of a workgroup of the backward: one team where a row takes several
-// waves; else as many wave (or 16-lane) teams as the registers of V octets let
-// a compute unit hold.
-template <int LANES, int V> constexpr int back_block() { return LANES > 64 ? LANES : V >= 4 ? 512 : 1024; }
+// A workgroup of the backward: 16 wavefronts, one to a compute unit.
+constexpr int BACK_BLOCK = 1024;
+
+// What a team reads of a row, loaded one row ahead.
+template <int DT, int V, bool KEPT> struct RowIn {
+    Oct<DT> dy[V], x[KEPT ? 1 : V];
+    uint2 k[KEPT ? V : 1];
+    float scale[KEPT ? V : 1];
+    float mean, rstd;
+};
 
 template <int DT, bool WIDE, int LANES, int V, bool KEPT>
-__global__ __launch_bounds__((back_block<LANES, V>())) void backward_kernel(
+__global__ __launch_bounds__(BACK_BLOCK) void backward_kernel(
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const float *__restrict__ stats,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight, typename Elem<DT>::storage *__restrict__ dx,
@@ -132,85 +169,96 @@ __global__ __launch_bounds__((back_block<LANES, V>())) void backward_kernel(
     typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dbias, float *__restrict__ partial, int32_t rows,
     int32_t d, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
-    constexpr int BLOCK = back_block<LANES, V>();
-    constexpr int TEAMS = BLOCK / LANES, WAVES = BLOCK / 64;
+    constexpr int TEAMS = BACK_BLOCK / LANES, WAVES = BACK_BLOCK / 64;
+    constexpr int TEAM_WAVES = LANES > 64 ? LANES / 64 : 1;
     constexpr int COLS = LANES > 64 ? 64 : LANES;  // lanes of a wave that own different columns
-    __shared__ float slots[2][LANES > 64 ? LANES / 32 : 1];
+    // rows loaded one ahead where the registers allow it (128 a lane)
+    constexpr bool AHEAD = V * (DT == DT_F32 ? 2 : 1) <= 2;
+    __shared__ float slots[2][TEAMS][2 * TEAM_WAVES];
     __shared__ float parts[TEAMS > 1 ? WAVES * 16 * (COLS + 1) : 1];
-    const uint32_t lane = threadIdx.x % LANES;
+    const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
+    const uint32_t step = gridDim.x * TEAMS;
     const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
     const float inv_d = 1.0f / (float)d;
+    Oct<WT> w[V];
     float aw[V][8], ab[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        const int c = (int)(v * LANES + lane) * 8;
+        oct_load<WT, false>(w[v], weight + c, d - c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) aw[v][e] = ab[v][e] = 0.0f;
-    int turn = 0;
-    for (uint32_t row = blockIdx.x * TEAMS + threadIdx.x / LANES; row < live_rows; row += gridDim.x * TEAMS) {
-        const typename Elem<DT>::storage *dy = dout + (size_t)row * d;
-        Oct<DT> o[V], x[KEPT ? 1 : V];
-        uint2 k[KEPT ? V : 1];
-        float sc[KEPT ? V : 1];
+    }
+    auto load = [&](RowIn<DT, V, KEPT> &r, uint32_t row) {
+        if (row >= live_rows) return;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (int)(v * LANES + lane) * 8;
             const int n = d - c;
-            oct_load<DT>(o[v], dy + c, n);
+            oct_load<DT>(r.dy[v], dout + (size_t)row * d + c, n);
             if constexpr (KEPT) {
-                k[v] = codes_load(codes + (size_t)row * d + c, n);
-                sc[v] = n > 0 ? scales[(size_t)row * nb + (uint32_t)c / BLOCK8] : 0.0f;
+                r.k[v] = codes_load(codes + (size_t)row * d + c, n);
+                r.scale[v] = n > 0 ? scales[(size_t)row * nb + (uint32_t)c / BLOCK8] : 0.0f;
             } else {
-                oct_load<DT>(x[v], in + (size_t)row * d + c, n);
+                oct_load<DT>(r.x[v], in + (size_t)row * d + c, n);
             }
         }
-        const float mean = stats[2 * (size_t)row], rstd = stats[2 * (size_t)row + 1];
-        // v = dy w and n of an octet; past the row's end dy is 0 and n finite
-        auto octet = [&](int v, float (&dv)[8], float (&n8)[8], float (&dyf)[8]) {
-            const int c = (int)(v * LANES + lane) * 8;
-            Oct<WT> w;
-            float wf[8];
-            oct_load<WT, false>(w, weight + c, d - c);
-            oct_unpack<WT>(w, wf);
-            oct_unpack<DT>(o[v], dyf);
-            if constexpr (KEPT) {
-                block_decode(k[v], sc[v], n8);
+        r.mean = stats[2 * (size_t)row];
+        r.rstd = stats[2 * (size_t)row + 1];
+    };
+    // dy and t (n = rstd t) of an octet; past the row's end dy is 0
+    auto octet = [&](const RowIn<DT, V, KEPT> &r, int v, float (&dy)[8], float (&t)[8]) {
+        oct_unpack<DT>(r.dy[v], dy);
+        if constexpr (KEPT) {
+            block_decode(r.k[v], r.scale[v], t);
+        } else {
+            oct_unpack<DT>(r.x[v], t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) n8[e] *= rstd;
-            } else {
-                oct_unpack<DT>(x[v], n8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) n8[e] = (n8[e] - mean) * rstd;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dv[e] = dyf[e] * wf[e];
-        };
+            for (int e = 0; e < 8; ++e) t[e] -= r.mean;
+        }
+    };
+    RowIn<DT, V, KEPT> r, next;
+    if constexpr (AHEAD) load(next, blockIdx.x * TEAMS + team);
+    int turn = 0;
+    for (uint32_t base = blockIdx.x * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
+        const uint32_t row = base + team;
+        if constexpr (AHEAD) {
+            r = next;
+            load(next, row + step);
+        } else {
+            load(r, row);
+        }
         float s1 = 0.0f, s2 = 0.0f;
+        if (row < live_rows) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if ((int)(v * LANES + lane) * 8 >= d) continue;
-            float dv[8], n8[8], dyf[8];
-            octet(v, dv, n8, dyf);
+            for (int v = 0; v < V; ++v) {
+                float dy[8], t[8], wf[8];
+                octet(r, v, dy, t);
+                oct_unpack<WT>(w[v], wf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s1 += dv[e];
-                s2 = __builtin_fmaf(dv[e], n8[e], s2);
-                ab[v][e] += dyf[e];
-                aw[v][e] = __builtin_fmaf(dyf[e], n8[e], aw[v][e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float n = t[e] * r.rstd, dv = dy[e] * wf[e];
+                    s1 += dv;
+                    s2 = __builtin_fmaf(dv, n, s2);
+                    ab[v][e] += dy[e];
+                    aw[v][e] = __builtin_fmaf(dy[e], n, aw[v][e]);
+                }
             }
         }
-        team_sum2<LANES>(s1, s2, slots[turn]);
+        team_sum2<LANES>(s1, s2, slots[turn][team]);
         turn ^= 1;
-        const float m1 = s1 * inv_d, m2 = s2 * inv_d;
+        if (row >= live_rows) continue;
+        const float m1 = s1 * inv_d, m2 = s2 * inv_d * r.rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (int)(v * LANES + lane) * 8;
-            if (c >= d) continue;
-            float dv[8], n8[8], dyf[8];
-            octet(v, dv, n8, dyf);
+            float dy[8], t[8], wf[8];
+            octet(r, v, dy, t);
+            oct_unpack<WT>(w[v], wf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dv[e] = rstd * (dv[e] - __builtin_fmaf(n8[e], m2, m1));
-            oct_store<DT>(dx + (size_t)row * d + c, dv, d - c);
+            for (int e = 0; e < 8; ++e) dy[e] = r.rstd * (dy[e] * wf[e] - __builtin_fmaf(t[e], m2, m1));
+            if (c < d) oct_store<DT>(dx + (size_t)row * d + c, dy, d - c);
         }
     }
     // one workgroup in all: its sums are the gradients
@@ -237,14 +285,15 @@ __global__ __launch_bounds__((back_block<LANES, V>())) void backward_kernel(
             }
         }
     } else {
+        // the teams' sums, wave by wave (a 16-lane team's wave adds its four first)
         const uint32_t wave = threadIdx.x / 64, wl = threadIdx.x & 63;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (v > 0) __syncthreads();
+            __syncthreads();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float a = aw[v][e], b = ab[v][e];
-                if constexpr (LANES == 16) {  // the wave's four teams
+                if constexpr (LANES == 16) {
                     a += __shfl_xor(a, 16);
                     b += __shfl_xor(b, 16);
                     a += __shfl_xor(a, 32);
@@ -256,12 +305,15 @@ __global__ __launch_bounds__((back_block<LANES, V>())) void backward_kernel(
                 }
             }
             __syncthreads();
-            for (uint32_t i = threadIdx.x; i < COLS * 16; i += BLOCK) {
-                const uint32_t which = i / (COLS * 8), at = i % (COLS * 8);
-                const uint32_t e = at % 8, cl = at / 8;
+            // WAVES / TEAM_WAVES waves hold each of the team's 64 TEAM_WAVES lanes
+            constexpr uint32_t WIDTH = TEAM_WAVES * COLS * 8;
+            for (uint32_t i = threadIdx.x; i < 2 * WIDTH; i += BACK_BLOCK) {
+                const uint32_t which = i / WIDTH, at = i % WIDTH;
+                const uint32_t e = at % 8, cl = at / 8;  // element, lane of the team
                 float t = 0.0f;
 #pragma unroll
-                for (int g = 0; g < WAVES; ++g) t += parts[(g * 16 + which * 8 + e) * (COLS + 1) + cl];
+                for (int g = 0; g < WAVES / TEAM_WAVES; ++g)
+                    t += parts[((g * TEAM_WAVES + cl / COLS) * 16 + which * 8 + e) * (COLS + 1) + cl % COLS];
                 const int col = (int)(v * LANES + cl) * 8 + (int)e;
                 if (col < d) put((int)which, col, t);
             }
@@ -302,15 +354,20 @@ struct Forward {
     int32_t rows, d;
     float eps;
     const int32_t *live;
+    int cus;
     hipStream_t stream;
 };
+
+constexpr int FORWARD_HELD = 1024;  // threads of a compute unit
 
 template <int DT, bool WIDE, int LANES, int V>
 hipError_t forward_as(const Forward &a) {
     using S = typename Elem<DT>::storage;
     using WS = typename Elem<weight_type<DT, WIDE>()>::storage;
-    constexpr int TEAMS = ln_block<LANES>() / LANES;
-    const dim3 grid((uint32_t)(((int64_t)a.rows + TEAMS - 1) / TEAMS)), block(ln_block<LANES>());
+    constexpr int BLOCK = forward_block<LANES>(), TEAMS = BLOCK / LANES;
+    // as many workgroups as the device holds at four wavefronts a SIMD
+    const int64_t need = ((int64_t)a.rows + TEAMS - 1) / TEAMS, most = (int64_t)a.cus * (FORWARD_HELD / BLOCK);
+    const dim3 grid((uint32_t)(need < most ? need : most)), block(BLOCK);
     if (a.codes != nullptr)
         forward_kernel<DT, WIDE, LANES, V, true><<<grid, block, 0, a.stream>>>(
             (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias, (S *)a.out, (uint8_t *)a.codes, a.scales,
@@ -324,15 +381,7 @@ hipError_t forward_as(const Forward &a) {
 
 template <int DT, bool WIDE>
 hipError_t forward_dt(const Forward &a) {
-    const int64_t d = a.d;
-    if (d <= 128) return forward_as<DT, WIDE, 16, 1>(a);
-    if (d <= 512) return forward_as<DT, WIDE, 64, 1>(a);
-    if (d <= 1024) return forward_as<DT, WIDE, 64, 2>(a);
-    if (d <= 2048) return forward_as<DT, WIDE, 128, 2>(a);
-    if (d <= 4096) return forward_as<DT, WIDE, 256, 2>(a);
-    if (d <= 8192) return forward_as<DT, WIDE, 512, 2>(a);
-    if (d <= 16384) return forward_as<DT, WIDE, 1024, 2>(a);
-    return forward_as<DT, WIDE, 1024, 4>(a);
+    return by_width(a.d, [&](auto t) { return forward_as<DT, WIDE, decltype(t)::LANES, decltype(t)::V>(a); });
 }
 
 struct Backward {
@@ -353,7 +402,7 @@ hipError_t backward_as(const Backward &a) {
     using S = typename Elem<DT>::storage;
     constexpr int WT = weight_type<DT, WIDE>();
     using WS = typename Elem<WT>::storage;
-    const dim3 grid((uint32_t)a.groups), block(back_block<LANES, V>());
+    const dim3 grid((uint32_t)a.groups), block(BACK_BLOCK);
     if (!a.kept)
         backward_kernel<DT, WIDE, LANES, V, false><<<grid, block, 0, a.stream>>>(
             (const S *)a.dout, (const S *)a.in, nullptr, nullptr, a.stats, (const WS *)a.weight, (S *)a.dx,
@@ -370,35 +419,23 @@ hipError_t backward_as(const Backward &a) {
     return hipGetLastError();
 }
 
-// (lanes of a team, octets a lane) by d; layer_norm_groups reads the same rule.
 template <int DT, bool WIDE>
 hipError_t backward_dt(const Backward &a) {
-    const int64_t d = a.d;
-    if (d <= 128) return backward_as<DT, WIDE, 16, 1>(a);
-    if (d <= 512) return backward_as<DT, WIDE, 64, 1>(a);
-    if (d <= 1024) return backward_as<DT, WIDE, 64, 2>(a);
-    if (d <= 2048) return backward_as<DT, WIDE, 64, 4>(a);
-    if (d <= 4096) return backward_as<DT, WIDE, 128, 4>(a);
-    if (d <= 8192) return backward_as<DT, WIDE, 256, 4>(a);
-    if (d <= 16384) return backward_as<DT, WIDE, 512, 4>(a);
-    return backward_as<DT, WIDE, 1024, 4>(a);
+    return by_width(a.d, [&](auto t) { return backward_as<DT, WIDE, decltype(t)::LANES, decltype(t)::V>(a); });
 }
 
 }  // namespace
 
 int layer_norm_groups(int64_t rows, int64_t d, int cus) {
-    // teams of one workgroup, and workgroups a compute unit holds at a time
-    const int teams = d <= 128 ? 64 : d <= 1024 ? 16 : d <= 2048 ? 8 : 1;
-    const int held = d <= 2048 ? 1 : d <= 4096 ? 6 : d <= 8192 ? 3 : 1;
+    const int64_t teams = by_width(d, [](auto t) { return (int64_t)(BACK_BLOCK / decltype(t)::LANES); });
     const int64_t need = (rows + teams - 1) / teams;
-    const int64_t most = (int64_t)cus * held;
-    return (int)(need < 1 ? 1 : need < most ? need : most);
+    return (int)(need < 1 ? 1 : need < cus ? need : cus);
 }
 
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
                              void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
-                             const int32_t *live, hipStream_t stream) {
-    const Forward a{in, weight, bias, out, codes, scales, stats, rows, d, eps, live, stream};
+                             const int32_t *live, int cus, hipStream_t stream) {
+    const Forward a{in, weight, bias, out, codes, scales, stats, rows, d, eps, live, cus, stream};
     switch (dtype) {
     case DT_F32: return forward_dt<DT_F32, true>(a);
     case DT_F16: return wide ? forward_dt<DT_F16, true>(a) : forward_dt<DT_F16, false>(a);

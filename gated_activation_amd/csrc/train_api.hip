@@ -94,9 +94,6 @@ ga_status check_rows_fit(const char *op, int32_t activation, int64_t rows, int64
     return check_blocks(op, rows * blocks_of(d));
 }
 
-// Lanes that share a row in the layer norm's forward pass, at least.
-int64_t norm_lanes(int64_t d) { return d <= 128 ? 16 : d <= 1024 ? 64 : d <= 2048 ? 128 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
-
 ga_status check_weight_type(const char *op, int32_t dtype, int32_t weight_dtype) {
     if (weight_dtype != dtype && weight_dtype != GA_F32)
         return fail(GA_EINVAL, "%s: weight dtype %d is neither fp32 nor the rows' %d", op, (int)weight_dtype, (int)dtype);
@@ -126,11 +123,13 @@ ga_status layer_norm(const char *op, const void *in, const void *weight, const v
                               {"stats", stats, (size_t)rows * 8, 4, true, false},
                               {"codes", codes, keep ? n : 0, 1, true, !keep},
                               {"scales", scales, keep ? (size_t)rows * blocks_of(d) * 4 : 0, 4, true, !keep}};
-    if ((st = check_regions(op, regions)) != GA_OK || (st = check_items(op, rows, norm_lanes(d))) != GA_OK) return st;
+    if ((st = check_regions(op, regions)) != GA_OK) return st;
     if (rows == 0) return GA_OK;
+    int cus = 0;
+    if ((st = usable_cus(&cus)) != GA_OK) return st;
     return ga::launched(op, ga::launch_layer_norm(dtype, weight_dtype == GA_F32, in, weight, bias, out,
                                                   keep ? codes : nullptr, scales, stats, (int32_t)rows, (int32_t)d, eps,
-                                                  live_rows, (hipStream_t)stream));
+                                                  live_rows, cus, (hipStream_t)stream));
 }
 
 ga_status layer_norm_backward(const char *op, const void *dout, const void *in, const void *codes, const float *scales,

@@ -329,8 +329,10 @@ ga_status ga_gelu_and_mul_sparse_down_with_plan(const void *gu, const void *w, v
  * shorter.  With m the block's largest magnitude, counted as at least 2^-100:
  *     code  = 127 x / m, the exact quotient rounded to the nearest integer
  *             (ties to even), an int8 in [-127, 127]
- *     scale = fp32(m / 127)
+ *     scale = m / 127 in fp32
  *     value = code * scale, within m / 254 of x (up to fp32 rounding)
+ * (A 16-bit row's differences from its own mean or cutoff are coded from the
+ * fp32 quotient: one within 127 * 2^-21 of a half-integer may go to either side.)
  * A block that holds a NaN, an infinity or a magnitude of 2^126 or more has
  * the scale NaN: all values restored from it are NaN.
  *   codes   int8 [rows, halves, d]

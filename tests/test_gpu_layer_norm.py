@@ -68,10 +68,12 @@ def test_forward_and_backward(dtype, wide, rows, d, offset, live):
     assert torch.equal(st[:n], st2[:n])
     t32 = (xe - mean).astype(np.float32).astype(np.float64)
     wc, ws, q = ref.encode(t32)
-    near = np.abs(np.abs(q - np.rint(q)) - 0.5) < 1e-6     # fp64 means may differ in their last bits
+    # fp64 means may differ in their last bits; 16-bit rows form x - mean in two fp32 roundings and the
+    # quotient in fp32: 2 u of x - mean (and of the block's largest) and 2^-22 of the quotient, up to 127
+    near = np.abs(np.abs(q - np.rint(q)) - 0.5) < (1e-6 if dtype == "fp32" else 127 * (2 * 2 * ref.U + 2.0 ** -22) + 1e-6)
     got = k[:n].cpu().numpy()
     assert np.array_equal(got[~near], wc[~near]) and (np.abs(got.astype(int) - wc) <= 1).all(), label
-    close(s[:n], ws, 3 * ref.U * ws + 1e-14, label + " scales")
+    close(s[:n], ws, 5 * ref.U * ws + 1e-14, label + " scales")
     # terms a lane adds in a row's sums: 8 an octet, at most 4 octets
     st64 = st[:n].double().cpu().numpy()
     grads, bounds = ref.layer_norm_backward(de, (xe - st64[:, :1]) * st64[:, 1:], st64[:, 1:], we, dtype, wdtype, 32)
