@@ -151,11 +151,12 @@ constexpr int64_t LN_MAX_D = 32768;
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
                              void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
                              const int32_t *live, int cus, hipStream_t stream);
-// Workgroups of the backward's first launch, each of which leaves one partial
-// row of the weight's and the bias' gradient in the workspace ([groups, 2, d]
-// fp32; unused when there is one group).  kept: from codes and scales, else
-// from in.
+// Groups of rows in the backward's launch, each of which leaves one partial row
+// of the weight's and the bias' gradient in the workspace ([groups, 2, d] fp32;
+// none with one group), after two sums for each strip of rows that are cut into
+// strips.  kept: from codes and scales, else from in.
 int layer_norm_groups(int64_t rows, int64_t d, int cus);
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups);
 hipError_t launch_layer_norm_backward(int dtype, bool wide, const void *dout, const void *in, const void *codes,
                                       const float *scales, const float *stats, const void *weight, void *dx,
                                       void *dweight, void *dbias, bool kept, int32_t rows, int32_t d,

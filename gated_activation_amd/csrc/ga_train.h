@@ -130,6 +130,71 @@ __device__ __forceinline__ void codes_store(uint8_t *p, uint2 c, int n) {
 }
 
 // ---------------------------------------------------------------------------
+// The same for kernels that hold a row in registers and load ahead.  A branch
+// around a load makes the compiler wait for it where the paths meet, so these
+// loads have none: fetch reads the eight elements from column c, or where they
+// would pass the row's end the row's last eight, and trim, called when the
+// octet is used, moves a partial octet's elements into place and clears the
+// rest (all of an octet past the end).  TINY rows (d < 8) go element by
+// element.
+// ---------------------------------------------------------------------------
+template <int DT, bool TINY, bool NT = true>
+__device__ __forceinline__ void oct_fetch(Oct<DT> &o, const typename Elem<DT>::storage *row, int c, int d) {
+    if constexpr (TINY) oct_load<DT, NT>(o, row + c, d - c);
+    else oct_load<DT, NT>(o, row + (c < d - 8 ? c : d - 8), 8);
+}
+
+// Words i take words i + K where `on`, and 0 past the last.
+template <int K, int DT>
+__device__ __forceinline__ void words_down(Oct<DT> &o, bool on) {
+#pragma unroll
+    for (int i = 0; i < Oct<DT>::WORDS; ++i) {
+        const uint32_t from = i + K < Oct<DT>::WORDS ? o.w[i + K < Oct<DT>::WORDS ? i + K : 0] : 0u;
+        o.w[i] = on ? from : o.w[i];
+    }
+}
+
+template <int DT, bool TINY>
+__device__ __forceinline__ void oct_trim(Oct<DT> &o, int c, int d) {
+    if constexpr (!TINY) {
+        const int s = c - (d - 8);  // elements to drop
+        if (s > 0) {
+            if constexpr (DT == DT_F32) {
+                words_down<4>(o, (s & 4) != 0);
+                words_down<2>(o, (s & 2) != 0);
+                words_down<1>(o, (s & 1) != 0);
+            } else {
+                words_down<2>(o, (s & 4) != 0);
+                words_down<1>(o, (s & 2) != 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t from = o.w[i] >> 16 | (i < 3 ? o.w[i < 3 ? i + 1 : 0] << 16 : 0u);
+                    o.w[i] = (s & 1) != 0 ? from : o.w[i];
+                }
+            }
+            if (s >= 8) oct_zero(o);
+        }
+    }
+}
+
+template <bool TINY>
+__device__ __forceinline__ uint2 codes_fetch(const uint8_t *row, int c, int d) {
+    if constexpr (TINY) return codes_load(row + c, d - c);
+    else return codes_load(row + (c < d - 8 ? c : d - 8), 8);
+}
+
+template <bool TINY>
+__device__ __forceinline__ void codes_trim(uint2 &k, int c, int d) {
+    if constexpr (!TINY) {
+        if (c > d - 8) {
+            const int s = c - (d - 8);
+            const uint64_t v = s >= 8 ? 0 : ((uint64_t)k.y << 32 | k.x) >> (8 * s);
+            k = uint2{(uint32_t)v, (uint32_t)(v >> 32)};
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The 8-bit block code.  For a block of up to 128 values with largest
 // magnitude m (counted as at least 2^-100):
 //     code = round-half-even(127 x / m), the exact quotient,

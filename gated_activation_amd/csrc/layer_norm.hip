@@ -21,6 +21,8 @@
 // launch adds the workgroups' partials, again in a fixed order, so the result
 // does not depend on scheduling.  One workgroup per compute unit keeps those
 // partials at 8 d bytes times 256.
+#include <type_traits>
+
 #include "ga_internal.h"
 #include "ga_train.h"
 
@@ -34,12 +36,14 @@ template <int DT, bool WIDE> constexpr int weight_type() { return WIDE ? DT_F32 
 // The team of a row by its width: LANES lanes of V octets.  Two octets a lane
 // halve what the row's reductions cost a value; a row of up to 1024 values is
 // a wavefront's own and needs no barrier.
-template <int LANES_, int V_> struct Team {
+template <int LANES_, int V_, bool TINY_ = false> struct Team {
     static constexpr int LANES = LANES_, V = V_;
+    static constexpr bool TINY = TINY_;  // rows of fewer than eight values
 };
 
 template <typename F>
 auto by_width(int64_t d, F &&f) {
+    if (d < 8) return f(Team<16, 1, true>());
     if (d <= 128) return f(Team<16, 1>());
     if (d <= 512) return f(Team<64, 1>());
     if (d <= 1024) return f(Team<64, 2>());
@@ -50,220 +54,301 @@ auto by_width(int64_t d, F &&f) {
     return f(Team<1024, 4>());
 }
 
-constexpr int FORWARD_BLOCK = 256;  // workgroups of several teams; a larger team is one by itself
+constexpr int FORWARD_BLOCK = 128;  // workgroups of several teams; a larger team is one by itself
 template <int LANES> constexpr int forward_block() { return LANES > FORWARD_BLOCK ? LANES : FORWARD_BLOCK; }
 
-// One row of a team, and the rows its workgroup's teams take in turn.
-template <int DT, bool WIDE, int LANES, int V, bool KEEP>
-__global__ __launch_bounds__(forward_block<LANES>(), 4) void forward_kernel(
+// One row to a team.  Rows come and go with the workgroups, so a wavefront's
+// stores never hold up a load; all of a row's loads are issued at once.
+template <int DT, bool WIDE, typename T, bool KEEP>
+__global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
     const typename Elem<DT>::storage *__restrict__ in,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ bias, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
     float eps, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
+    constexpr int LANES = T::LANES, V = T::V;
+    constexpr bool TINY = T::TINY;
     constexpr int TEAMS = forward_block<LANES>() / LANES, WAVES = LANES > 64 ? LANES / 64 : 1;
-    __shared__ double slots[2][TEAMS][2 * WAVES];
+    __shared__ double slots[TEAMS][2 * WAVES];
     const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
-    const uint32_t step = gridDim.x * TEAMS;
     const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
+    if (blockIdx.x * TEAMS >= live_rows) return;
+    const bool mine = blockIdx.x * TEAMS + team < live_rows;  // a team without a row follows the last one
+    const uint32_t row = mine ? blockIdx.x * TEAMS + team : live_rows - 1;
+    const typename Elem<DT>::storage *x = in + (size_t)row * d;
+    Oct<DT> o[V];
     Oct<WT> w[V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) oct_fetch<DT, TINY>(o[v], x, (int)(v * LANES + lane) * 8, d);
+    const float first = Elem<DT>::to_f32(x[0]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        oct_fetch<WT, TINY, false>(w[v], weight, (int)(v * LANES + lane) * 8, d);
+        oct_fetch<WT, TINY, false>(b[v], bias != nullptr ? bias : weight, (int)(v * LANES + lane) * 8, d);
+    }
+    double s1 = 0.0, s2 = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * LANES + lane) * 8;
-        oct_load<WT, false>(w[v], weight + c, d - c);
-        if (bias != nullptr) oct_load<WT, false>(b[v], bias + c, d - c);
-        else oct_zero(b[v]);
-    }
-    Oct<DT> next[V];
-    float next_first = 0.0f;
-    auto load = [&](uint32_t row) {
-        if (row >= live_rows) return;
-        const typename Elem<DT>::storage *x = in + (size_t)row * d;
+        const int n = d - c;
+        float f[8];
+        oct_trim<DT, TINY>(o[v], c, d);
+        oct_unpack<DT>(o[v], f);
+        if (n < 8) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * LANES + lane) * 8;
-            oct_load<DT>(next[v], x + c, d - c);
+            for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : first;
         }
-        next_first = Elem<DT>::to_f32(x[0]);
-    };
-    load(blockIdx.x * TEAMS + team);
-    int turn = 0;
-    for (uint32_t base = blockIdx.x * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
-        const uint32_t row = base + team;
-        Oct<DT> o[V];
+        add_shifted<DT>(f, first, s1, s2);
+    }
+    team_sum2<LANES>(s1, s2, slots[team]);
+    if (!mine) return;
+    double m, var;
+    shifted_moments(s1, s2, (double)first, (double)d, m, var);
+    const RowOrigin<DT> mean(m);
+    const float rstd = (float)(1.0 / __builtin_sqrt(var + (double)eps));
+    if (lane == 0) {
+        stats[2 * (size_t)row] = mean.hi;
+        stats[2 * (size_t)row + 1] = rstd;
+    }
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = next[v];
-        const float first = next_first;
-        load(row + step);
-        double s1 = 0.0, s2 = 0.0;
+    for (int v = 0; v < V; ++v) {
+        const int c = (int)(v * LANES + lane) * 8;
+        const int n = d - c;
+        const uint32_t block = (uint32_t)c / BLOCK8;
+        if (block >= nb) continue;  // the same for the 16 lanes of a block
+        float f[8], wf[8], bf[8];
+        oct_unpack<DT>(o[v], f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int n = d - (int)(v * LANES + lane) * 8;
-            float f[8];
-            oct_unpack<DT>(o[v], f);
+        for (int e = 0; e < 8; ++e) f[e] = mean.from(f[e]);
+        if constexpr (KEEP) {
             if (n < 8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : first;
+                for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : 0.0f;
             }
-            add_shifted<DT>(f, first, s1, s2);
+            float scale;
+            const uint2 k = block_encode<difference_of<DT>(), false>(f, scale);
+            codes_store(codes + (size_t)row * d + c, k, n);
+            if ((lane & 15) == 0) scales[(size_t)row * nb + block] = scale;
         }
-        team_sum2<LANES>(s1, s2, slots[turn][team]);
-        turn ^= 1;
-        if (row >= live_rows) continue;
-        double m, var;
-        shifted_moments(s1, s2, (double)first, (double)d, m, var);
-        const RowOrigin<DT> mean(m);
-        const float rstd = (float)(1.0 / __builtin_sqrt(var + (double)eps));
-        if (lane == 0) {
-            stats[2 * (size_t)row] = mean.hi;
-            stats[2 * (size_t)row + 1] = rstd;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * LANES + lane) * 8;
-            const int n = d - c;
-            const uint32_t block = (uint32_t)c / BLOCK8;
-            if (block >= nb) continue;  // the same for the 16 lanes of a block
-            float f[8], wf[8], bf[8];
-            oct_unpack<DT>(o[v], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = mean.from(f[e]);
-            if constexpr (KEEP) {
-                if (n < 8) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : 0.0f;
-                }
-                float scale;
-                const uint2 k = block_encode<difference_of<DT>(), false>(f, scale);
-                codes_store(codes + (size_t)row * d + c, k, n);
-                if ((lane & 15) == 0) scales[(size_t)row * nb + block] = scale;
-            }
-            oct_unpack<WT>(w[v], wf);
+        oct_trim<WT, TINY>(w[v], c, d);
+        oct_unpack<WT>(w[v], wf);
+        if (bias != nullptr) {
+            oct_trim<WT, TINY>(b[v], c, d);
             oct_unpack<WT>(b[v], bf);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, wf[e], bf[e]);
-            oct_store<DT>(out + (size_t)row * d + c, f, n);
+            for (int e = 0; e < 8; ++e) bf[e] = 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, wf[e], bf[e]);
+        oct_store<DT>(out + (size_t)row * d + c, f, n);
     }
 }
 
-// A workgroup of the backward: 16 wavefronts, one to a compute unit.
-constexpr int BACK_BLOCK = 1024;
+// A workgroup of the backward: eight wavefronts of up to 256 registers, one
+// workgroup to a compute unit.
+constexpr int BACK_BLOCK = 512;
 
-// What a team reads of a row, loaded one row ahead.
+template <typename F>
+auto by_width_backward(int64_t d, F &&f) {
+    if (d < 8) return f(Team<16, 1, true>());
+    if (d <= 128) return f(Team<16, 1>());
+    if (d <= 512) return f(Team<64, 1>());
+    if (d <= 1024) return f(Team<64, 2>());
+    if (d <= 2048) return f(Team<128, 2>());
+    if (d <= 4096) return f(Team<256, 2>());
+    return f(Team<512, 2>());
+}
+
+// Rows wider than a workgroup's 512 lanes of two octets are cut into strips of
+// STRIP columns and read twice: SUMS leaves each strip's part of a row's two
+// sums in the workspace, APPLY adds a row's parts and does the rest for its
+// strip's columns.  (Four and eight octets a lane, one pass, spilled: 2048 rows
+// of 16384, bf16 from codes, took 80 us, 1024 rows of 32768 414 us, against
+// 62 us either way.)
+constexpr int STRIP = 8192;
+enum Stage { WHOLE, SUMS, APPLY };
+constexpr int64_t strips_of(int64_t d) { return (d + STRIP - 1) / STRIP; }
+
+// Rows a team has in flight beside the one it works on, as the registers allow.
+template <int DT, int V> constexpr int rows_ahead() { return V * (DT == DT_F32 ? 2 : 1) <= 2 ? 1 : 0; }
+
+// What a team reads of a row.
 template <int DT, int V, bool KEPT> struct RowIn {
     Oct<DT> dy[V], x[KEPT ? 1 : V];
     uint2 k[KEPT ? V : 1];
-    float scale[KEPT ? V : 1];
+    float scale[KEPT ? V : 1], before[KEPT ? V : 1];  // of the octet's block, and of its first element's
     float mean, rstd;
 };
 
-template <int DT, bool WIDE, int LANES, int V, bool KEPT>
-__global__ __launch_bounds__(BACK_BLOCK) void backward_kernel(
+// The loop over rows has no branch around a load or a store: such a branch
+// makes the compiler wait for all of them wherever its paths meet, the stores
+// of the row before among them.  A lane whose octet passes the row's end works
+// on the row's last eight values instead: those of them that other lanes own
+// are left out of the sums, and stored with the very bits their owners store.
+// A team past the last row does that row again, out of the columns' sums.
+
+template <int DT, bool WIDE, typename T, bool KEPT, Stage STAGE>
+__global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const float *__restrict__ stats,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight, typename Elem<DT>::storage *__restrict__ dx,
     typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dweight,
-    typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dbias, float *__restrict__ partial, int32_t rows,
-    int32_t d, const int32_t *__restrict__ live) {
+    typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dbias, float *__restrict__ partial,
+    float2 *__restrict__ row_sums, int32_t rows, int32_t d, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
+    constexpr int LANES = T::LANES, V = T::V;
+    constexpr bool TINY = T::TINY;
     constexpr int TEAMS = BACK_BLOCK / LANES, WAVES = BACK_BLOCK / 64;
     constexpr int TEAM_WAVES = LANES > 64 ? LANES / 64 : 1;
     constexpr int COLS = LANES > 64 ? 64 : LANES;  // lanes of a wave that own different columns
-    // rows loaded one ahead where the registers allow it (128 a lane)
-    constexpr bool AHEAD = V * (DT == DT_F32 ? 2 : 1) <= 2;
+    constexpr int AHEAD = rows_ahead<DT, V>();
     __shared__ float slots[2][TEAMS][2 * TEAM_WAVES];
     __shared__ float parts[TEAMS > 1 ? WAVES * 16 * (COLS + 1) : 1];
     const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
-    const uint32_t step = gridDim.x * TEAMS;
+    // workgroups are numbered by group and strip
+    const uint32_t strips = STAGE == WHOLE ? 1 : (uint32_t)strips_of(d);
+    const uint32_t strip = STAGE == WHOLE ? 0 : blockIdx.x % strips;
+    const uint32_t group = STAGE == WHOLE ? blockIdx.x : blockIdx.x / strips;
+    const uint32_t groups = STAGE == WHOLE ? gridDim.x : gridDim.x / strips;
+    const int first = STAGE == WHOLE ? 0 : (int)strip * STRIP + (int)lane * 8;
+    auto column = [&](int v) { return STAGE == WHOLE ? (int)(v * LANES + lane) * 8 : first + v * LANES * 8; };
+    const uint32_t step = groups * TEAMS;
     const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
     const float inv_d = 1.0f / (float)d;
     Oct<WT> w[V];
     float aw[V][8], ab[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * LANES + lane) * 8;
-        oct_load<WT, false>(w[v], weight + c, d - c);
+        const int c = column(v);
+        oct_fetch<WT, TINY, false>(w[v], weight, c, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) aw[v][e] = ab[v][e] = 0.0f;
     }
     auto load = [&](RowIn<DT, V, KEPT> &r, uint32_t row) {
-        if (row >= live_rows) return;
+        row = row < live_rows ? row : live_rows - 1;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * LANES + lane) * 8;
-            const int n = d - c;
-            oct_load<DT>(r.dy[v], dout + (size_t)row * d + c, n);
+            const int c = column(v);
+            oct_fetch<DT, TINY>(r.dy[v], dout + (size_t)row * d, c, d);
             if constexpr (KEPT) {
-                r.k[v] = codes_load(codes + (size_t)row * d + c, n);
-                r.scale[v] = n > 0 ? scales[(size_t)row * nb + (uint32_t)c / BLOCK8] : 0.0f;
+                const uint32_t at = (uint32_t)(TINY || c < d - 8 ? c : d - 8), last = nb - 1;
+                const uint32_t block = (uint32_t)c / BLOCK8 < last ? (uint32_t)c / BLOCK8 : last;
+                r.k[v] = codes_fetch<TINY>(codes + (size_t)row * d, c, d);
+                r.scale[v] = scales[(size_t)row * nb + block];
+                r.before[v] = TINY ? 0.0f : scales[(size_t)row * nb + at / BLOCK8];
             } else {
-                oct_load<DT>(r.x[v], in + (size_t)row * d + c, n);
+                oct_fetch<DT, TINY>(r.x[v], in + (size_t)row * d, c, d);
             }
         }
         r.mean = stats[2 * (size_t)row];
         r.rstd = stats[2 * (size_t)row + 1];
     };
-    // dy and t (n = rstd t) of an octet; past the row's end dy is 0
+    // dy and t (n = rstd t) of an octet
     auto octet = [&](const RowIn<DT, V, KEPT> &r, int v, float (&dy)[8], float (&t)[8]) {
         oct_unpack<DT>(r.dy[v], dy);
         if constexpr (KEPT) {
             block_decode(r.k[v], r.scale[v], t);
+            // a last eight that begin in the block before the row's last
+            const int c = column(v), edge = (int)(nb - 1) * BLOCK8 - (d - 8);
+            if (!TINY && edge > 0 && c > d - 8) {
+                float u[8];
+                block_decode(r.k[v], r.before[v], u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = e < edge ? u[e] : t[e];
+            }
         } else {
             oct_unpack<DT>(r.x[v], t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] -= r.mean;
         }
     };
-    RowIn<DT, V, KEPT> r, next;
-    if constexpr (AHEAD) load(next, blockIdx.x * TEAMS + team);
+    auto dropped = [&](int v) {
+        const int s = column(v) - (d - 8);
+        return TINY || s < 0 ? 0 : s < 8 ? s : 8;
+    };
+    RowIn<DT, V, KEPT> r, next[AHEAD > 0 ? AHEAD : 1];
+    if (live_rows > 0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load(next[i], (group + i * groups) * TEAMS + team);
+    }
     int turn = 0;
-    for (uint32_t base = blockIdx.x * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
-        const uint32_t row = base + team;
-        if constexpr (AHEAD) {
-            r = next;
-            load(next, row + step);
+    for (uint32_t base = group * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
+        const bool mine = base + team < live_rows;
+        const uint32_t row = mine ? base + team : live_rows - 1;
+        if constexpr (AHEAD > 0) {
+            r = next[0];
+#pragma unroll
+            for (int i = 1; i < AHEAD; ++i) next[i - 1] = next[i];
+            load(next[AHEAD - 1], base + team + AHEAD * step);
         } else {
             load(r, row);
         }
         float s1 = 0.0f, s2 = 0.0f;
-        if (row < live_rows) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float dy[8], t[8], wf[8];
-                octet(r, v, dy, t);
-                oct_unpack<WT>(w[v], wf);
+        for (int v = 0; v < V; ++v) {
+            const int drop = dropped(v);  // elements that are other lanes'
+            float dy[8], t[8], wf[8];
+            octet(r, v, dy, t);
+            oct_unpack<WT>(w[v], wf);
+            if (drop > 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float n = t[e] * r.rstd, dv = dy[e] * wf[e];
-                    s1 += dv;
-                    s2 = __builtin_fmaf(dv, n, s2);
+                    dy[e] = e < drop ? 0.0f : dy[e];
+                    t[e] = e < drop ? 0.0f : t[e];
+                }
+            }
+            float a[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float n = t[e] * r.rstd, dv = dy[e] * wf[e];
+                s1 += dv;
+                s2 = __builtin_fmaf(dv, n, s2);
+                a[e] = n;
+            }
+            if (STAGE != SUMS && mine) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
                     ab[v][e] += dy[e];
-                    aw[v][e] = __builtin_fmaf(dy[e], n, aw[v][e]);
+                    aw[v][e] = __builtin_fmaf(dy[e], a[e], aw[v][e]);
                 }
             }
         }
-        team_sum2<LANES>(s1, s2, slots[turn][team]);
-        turn ^= 1;
-        if (row >= live_rows) continue;
+        if constexpr (STAGE == APPLY) {
+            s1 = s2 = 0.0f;
+            for (uint32_t i = 0; i < strips; ++i) {
+                const float2 p = row_sums[(size_t)row * strips + i];
+                s1 += p.x;
+                s2 += p.y;
+            }
+        } else {
+            team_sum2<LANES>(s1, s2, slots[turn][team]);
+            turn ^= 1;
+        }
+        if constexpr (STAGE == SUMS) {
+            if (lane == 0) row_sums[(size_t)row * strips + strip] = float2{s1, s2};
+            continue;
+        }
         const float m1 = s1 * inv_d, m2 = s2 * inv_d * r.rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * LANES + lane) * 8;
+            const int c = column(v);
             float dy[8], t[8], wf[8];
             octet(r, v, dy, t);
             oct_unpack<WT>(w[v], wf);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dy[e] = r.rstd * (dy[e] * wf[e] - __builtin_fmaf(t[e], m2, m1));
-            if (c < d) oct_store<DT>(dx + (size_t)row * d + c, dy, d - c);
+            if constexpr (TINY) oct_store<DT>(dx + (size_t)row * d + c, dy, d - c);
+            else oct_store<DT>(dx + (size_t)row * d + (c < d - 8 ? c : d - 8), dy, 8);
         }
     }
-    // one workgroup in all: its sums are the gradients
-    const bool last = gridDim.x == 1;
-    float *pw = partial + (size_t)blockIdx.x * 2 * d, *pb = pw + d;
+    if constexpr (STAGE == SUMS) return;
+    // one group in all: its sums are the gradients
+    const bool last = groups == 1;
+    float *pw = partial + (size_t)group * 2 * d, *pb = pw + d;
     auto put = [&](int which, int col, float v) {
         if (last) {
             if (which == 0) dweight[col] = Elem<WT>::from_f32(v);
@@ -275,12 +360,12 @@ __global__ __launch_bounds__(BACK_BLOCK) void backward_kernel(
     if constexpr (TEAMS == 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * LANES + lane) * 8;
+            const int c = column(v), drop = dropped(v), at = c < d - 8 ? c : d - 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (c + e < d) {
-                    put(0, c + e, aw[v][e]);
-                    put(1, c + e, ab[v][e]);
+                if (e >= drop) {
+                    put(0, at + e, aw[v][e]);
+                    put(1, at + e, ab[v][e]);
                 }
             }
         }
@@ -314,8 +399,9 @@ __global__ __launch_bounds__(BACK_BLOCK) void backward_kernel(
 #pragma unroll
                 for (int g = 0; g < WAVES / TEAM_WAVES; ++g)
                     t += parts[((g * TEAM_WAVES + cl / COLS) * 16 + which * 8 + e) * (COLS + 1) + cl % COLS];
-                const int col = (int)(v * LANES + cl) * 8 + (int)e;
-                if (col < d) put((int)which, col, t);
+                const int c = (int)(v * LANES + cl) * 8, drop = TINY ? 0 : c - (d - 8);
+                const int col = (drop > 0 ? d - 8 : c) + (int)e;
+                if ((int)e >= drop && col < d) put((int)which, col, t);
             }
         }
     }
@@ -358,22 +444,18 @@ struct Forward {
     hipStream_t stream;
 };
 
-constexpr int FORWARD_HELD = 1024;  // threads of a compute unit
-
-template <int DT, bool WIDE, int LANES, int V>
+template <int DT, bool WIDE, typename T>
 hipError_t forward_as(const Forward &a) {
     using S = typename Elem<DT>::storage;
     using WS = typename Elem<weight_type<DT, WIDE>()>::storage;
-    constexpr int BLOCK = forward_block<LANES>(), TEAMS = BLOCK / LANES;
-    // as many workgroups as the device holds at four wavefronts a SIMD
-    const int64_t need = ((int64_t)a.rows + TEAMS - 1) / TEAMS, most = (int64_t)a.cus * (FORWARD_HELD / BLOCK);
-    const dim3 grid((uint32_t)(need < most ? need : most)), block(BLOCK);
+    constexpr int BLOCK = forward_block<T::LANES>(), TEAMS = BLOCK / T::LANES;
+    const dim3 grid((uint32_t)(((int64_t)a.rows + TEAMS - 1) / TEAMS)), block(BLOCK);
     if (a.codes != nullptr)
-        forward_kernel<DT, WIDE, LANES, V, true><<<grid, block, 0, a.stream>>>(
+        forward_kernel<DT, WIDE, T, true><<<grid, block, 0, a.stream>>>(
             (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias, (S *)a.out, (uint8_t *)a.codes, a.scales,
             a.stats, a.rows, a.d, a.eps, a.live);
     else
-        forward_kernel<DT, WIDE, LANES, V, false><<<grid, block, 0, a.stream>>>(
+        forward_kernel<DT, WIDE, T, false><<<grid, block, 0, a.stream>>>(
             (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias, (S *)a.out, nullptr, nullptr, a.stats, a.rows,
             a.d, a.eps, a.live);
     return hipGetLastError();
@@ -381,7 +463,7 @@ hipError_t forward_as(const Forward &a) {
 
 template <int DT, bool WIDE>
 hipError_t forward_dt(const Forward &a) {
-    return by_width(a.d, [&](auto t) { return forward_as<DT, WIDE, decltype(t)::LANES, decltype(t)::V>(a); });
+    return by_width(a.d, [&](auto t) { return forward_as<DT, WIDE, decltype(t)>(a); });
 }
 
 struct Backward {
@@ -397,39 +479,57 @@ struct Backward {
     hipStream_t stream;
 };
 
-template <int DT, bool WIDE, int LANES, int V>
+template <int DT, bool WIDE, typename T>
 hipError_t backward_as(const Backward &a) {
     using S = typename Elem<DT>::storage;
     constexpr int WT = weight_type<DT, WIDE>();
     using WS = typename Elem<WT>::storage;
-    const dim3 grid((uint32_t)a.groups), block(BACK_BLOCK);
-    if (!a.kept)
-        backward_kernel<DT, WIDE, LANES, V, false><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, (const S *)a.in, nullptr, nullptr, a.stats, (const WS *)a.weight, (S *)a.dx,
-            (WS *)a.dweight, (WS *)a.dbias, a.workspace, a.rows, a.d, a.live);
-    else
-        backward_kernel<DT, WIDE, LANES, V, true><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, nullptr, (const uint8_t *)a.codes, a.scales, a.stats, (const WS *)a.weight, (S *)a.dx,
-            (WS *)a.dweight, (WS *)a.dbias, a.workspace, a.rows, a.d, a.live);
+    const int64_t strips = strips_of(a.d);
+    float2 *row_sums = (float2 *)a.workspace;
+    float *partial = a.workspace + (strips > 1 ? 2 * strips * a.rows : 0);
+    const dim3 grid((uint32_t)(a.groups * strips)), block(BACK_BLOCK);
+    auto launch = [&](auto kept, auto stage) {
+        constexpr bool KEPT = decltype(kept)::value;
+        backward_kernel<DT, WIDE, T, KEPT, decltype(stage)::value><<<grid, block, 0, a.stream>>>(
+            (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats, (const WS *)a.weight,
+            (S *)a.dx, (WS *)a.dweight, (WS *)a.dbias, partial, row_sums, a.rows, a.d, a.live);
+    };
+    auto launches = [&](auto kept) {
+        if constexpr (T::LANES == BACK_BLOCK) {
+            if (strips > 1) {
+                launch(kept, std::integral_constant<Stage, SUMS>());
+                launch(kept, std::integral_constant<Stage, APPLY>());
+                return;
+            }
+        }
+        launch(kept, std::integral_constant<Stage, WHOLE>());
+    };
+    if (a.kept) launches(std::true_type());
+    else launches(std::false_type());
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 1) return e;
     reduce_kernel<WT><<<dim3((uint32_t)((2 * a.d + REDUCE_COLS - 1) / REDUCE_COLS)),
-                        dim3(REDUCE_COLS * REDUCE_SLICES), 0, a.stream>>>(a.workspace, (WS *)a.dweight, (WS *)a.dbias,
+                        dim3(REDUCE_COLS * REDUCE_SLICES), 0, a.stream>>>(partial, (WS *)a.dweight, (WS *)a.dbias,
                                                                           a.groups, a.d);
     return hipGetLastError();
 }
 
 template <int DT, bool WIDE>
 hipError_t backward_dt(const Backward &a) {
-    return by_width(a.d, [&](auto t) { return backward_as<DT, WIDE, decltype(t)::LANES, decltype(t)::V>(a); });
+    return by_width_backward(a.d, [&](auto t) { return backward_as<DT, WIDE, decltype(t)>(a); });
 }
 
 }  // namespace
 
 int layer_norm_groups(int64_t rows, int64_t d, int cus) {
-    const int64_t teams = by_width(d, [](auto t) { return (int64_t)(BACK_BLOCK / decltype(t)::LANES); });
-    const int64_t need = (rows + teams - 1) / teams;
-    return (int)(need < 1 ? 1 : need < cus ? need : cus);
+    const int64_t teams = by_width_backward(d, [](auto t) { return (int64_t)(BACK_BLOCK / decltype(t)::LANES); });
+    const int64_t need = (rows + teams - 1) / teams, most = cus > strips_of(d) ? cus / strips_of(d) : 1;
+    return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups) {
+    const int64_t strips = strips_of(d);
+    return (groups > 1 ? (size_t)groups * 2 * (size_t)d * 4 : 0) + (strips > 1 ? (size_t)rows * (size_t)strips * 8 : 0);
 }
 
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,

@@ -305,8 +305,7 @@ ga_status ga_layer_norm_checkpoint(const void *in, const void *weight, const voi
 
 size_t ga_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
     if (rows < 1 || rows > INT32_MAX || d < 1 || d > ga::LN_MAX_D) return 0;
-    const int groups = ga::layer_norm_groups(rows, d, kMostCus);
-    return groups == 1 ? 0 : (size_t)groups * 2 * (size_t)d * 4;
+    return ga::layer_norm_workspace_bytes(rows, d, ga::layer_norm_groups(rows, d, kMostCus));
 }
 
 ga_status ga_layer_norm_backward(const void *dout, const void *in, const float *stats, const void *weight, void *dx,
