@@ -12,8 +12,7 @@
 // byte written once.  Work is numbered in blocks of 128 values of one row's
 // half; 16 consecutive lanes hold a block, eight values each, so its maximum
 // is four DPP steps.  A lane holds the octets of both halves at the same
-// column.  UNROLL independent blocks per lane keep several 16-byte loads in
-// flight.  The live count is read on the device and the grid comes from the
+// column.  The live count is read on the device and the grid comes from the
 // capacity alone, as in the forward-only kernels.
 #include "ga_internal.h"
 #include "ga_train.h"
@@ -25,6 +24,12 @@ namespace {
 constexpr int FLAT_BLOCK = 256;
 constexpr uint32_t FLAT_GROUPS = FLAT_BLOCK / 16;
 constexpr int OP_NONE = -1;
+
+// Blocks a 16-lane group has in flight.  Two where a block is one 16-byte load
+// a lane (4096 rows of 16384, bf16: store 31.8 us, 36.3 with one, 32.4 with
+// four); one where it is more (gelu forward, 8192 rows of 4096, bf16: 44.0 us,
+// 47.2 with two).
+template <int DT> constexpr int unroll_of(int halves) { return DT != DT_F32 && halves == 1 ? 2 : 1; }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
@@ -54,17 +59,24 @@ __device__ __forceinline__ void keep_block(const float (&x)[8], uint8_t *codes, 
 }
 
 // forward with checkpoint (ACT >= 0) and plain store (OP_NONE: no out, one half)
-template <int DT, int ACT, int UNROLL>
+template <int DT, int ACT, bool TINY>
 __global__ __launch_bounds__(FLAT_BLOCK) void store_kernel(
     const typename Elem<DT>::storage *__restrict__ in, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, int32_t rows_cap, uint32_t d, uint32_t nb, FastDiv by_nb,
     const int32_t *__restrict__ live) {
     constexpr bool GATED = ACT >= 0 && ACT != OP_SQUARED_RELU;
-    constexpr int H = GATED ? 2 : 1;
+    constexpr int H = GATED ? 2 : 1, UNROLL = unroll_of<DT>(H);
     const uint32_t rows = live != nullptr ? (uint32_t)clamp_live(live, rows_cap) : (uint32_t)rows_cap;
     const uint32_t total = rows * nb;
     const uint32_t step = gridDim.x * FLAT_GROUPS * UNROLL;
     const uint32_t l8 = (threadIdx.x & 15) * 8;
+    // a block's row and this lane's column; past the last block that one, unused
+    auto place = [&](uint32_t b, uint32_t &row, uint32_t &col, int &n) {
+        b = b < total ? b : total - 1;
+        row = by_nb(b);
+        col = (b - row * nb) * BLOCK8 + l8;
+        n = (int)d - (int)col;
+    };
     for (uint32_t base = blockIdx.x * FLAT_GROUPS * UNROLL + (threadIdx.x >> 4); base < total; base += step) {
         Oct<DT> g[UNROLL], u[UNROLL];
         uint32_t row[UNROLL], col[UNROLL];
@@ -72,20 +84,17 @@ __global__ __launch_bounds__(FLAT_BLOCK) void store_kernel(
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             const uint32_t b = base + k * FLAT_GROUPS;
-            row[k] = by_nb(b < total ? b : 0);
-            col[k] = (b - row[k] * nb) * BLOCK8 + l8;
-            n[k] = b < total ? (int)d - (int)col[k] : -1;
-            if (b < total) {
-                const size_t at = (size_t)row[k] * (H * d) + col[k];
-                oct_load<DT>(g[k], in + at, n[k]);
-                if constexpr (GATED) oct_load<DT>(u[k], in + at + d, n[k]);
-            }
+            place(b, row[k], col[k], n[k]);
+            const typename Elem<DT>::storage *x = in + (size_t)row[k] * (H * d);
+            oct_fetch<DT, TINY>(g[k], x, (int)col[k], (int)d);
+            if constexpr (GATED) oct_fetch<DT, TINY>(u[k], x + d, (int)col[k], (int)d);
         }
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             const uint32_t b = base + k * FLAT_GROUPS;
             if (b >= total) continue;
             float x[8], y[8];
+            oct_trim<DT, TINY>(g[k], (int)col[k], (int)d);
             oct_unpack<DT>(g[k], x);
             const size_t at = (size_t)row[k] * (H * d) + col[k];
             const size_t block = (size_t)row[k] * (H * nb) + (b - row[k] * nb);
@@ -95,6 +104,7 @@ __global__ __launch_bounds__(FLAT_BLOCK) void store_kernel(
                 for (int e = 0; e < 8; ++e) y[e] = act_value<ACT>(x[e]);
                 if constexpr (GATED) {
                     float up[8];
+                    oct_trim<DT, TINY>(u[k], (int)col[k], (int)d);
                     oct_unpack<DT>(u[k], up);
                     keep_block<DT>(up, codes + at + d, scales + block + nb, n[k], l8 == 0);
 #pragma unroll
@@ -108,15 +118,23 @@ __global__ __launch_bounds__(FLAT_BLOCK) void store_kernel(
 
 // codes * scale; `stats` (nullable): two floats for every `halves` rows, the
 // first of which is added to the first half (what the codes are relative to).
-template <int DT, int UNROLL>
+template <int DT, bool TINY>
 __global__ __launch_bounds__(FLAT_BLOCK) void restore_kernel(
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const float *__restrict__ stats,
     typename Elem<DT>::storage *__restrict__ out, int32_t rows_cap, uint32_t d, uint32_t nb, FastDiv by_nb,
     int32_t halves, const int32_t *__restrict__ live) {
+    constexpr int UNROLL = unroll_of<DT>(1);
     const uint32_t rows = (live != nullptr ? (uint32_t)clamp_live(live, rows_cap) : (uint32_t)rows_cap) * halves;
     const uint32_t total = rows * nb;
     const uint32_t step = gridDim.x * FLAT_GROUPS * UNROLL;
     const uint32_t l8 = (threadIdx.x & 15) * 8;
+    // a block's row and this lane's column; past the last block that one, unused
+    auto place = [&](uint32_t b, uint32_t &row, uint32_t &col, int &n) {
+        b = b < total ? b : total - 1;
+        row = by_nb(b);
+        col = (b - row * nb) * BLOCK8 + l8;
+        n = (int)d - (int)col;
+    };
     for (uint32_t base = blockIdx.x * FLAT_GROUPS * UNROLL + (threadIdx.x >> 4); base < total; base += step) {
         uint2 c[UNROLL];
         float scale[UNROLL], shift[UNROLL];
@@ -125,21 +143,18 @@ __global__ __launch_bounds__(FLAT_BLOCK) void restore_kernel(
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             const uint32_t b = base + k * FLAT_GROUPS;
-            row[k] = by_nb(b < total ? b : 0);
-            col[k] = (b - row[k] * nb) * BLOCK8 + l8;
-            n[k] = (int)d - (int)col[k];
+            place(b, row[k], col[k], n[k]);
+            scale[k] = scales[b < total ? b : total - 1];
+            c[k] = codes_fetch<TINY>(codes + (size_t)row[k] * d, (int)col[k], (int)d);
             shift[k] = 0.0f;
-            if (b < total) {
-                scale[k] = scales[b];
-                c[k] = codes_load(codes + (size_t)row[k] * d + col[k], n[k]);
-                if (stats != nullptr && (halves == 1 || (row[k] & 1) == 0))
-                    shift[k] = stats[2 * (size_t)(halves == 1 ? row[k] : row[k] >> 1)];
-            }
+            if (stats != nullptr && (halves == 1 || (row[k] & 1) == 0))
+                shift[k] = stats[2 * (size_t)(halves == 1 ? row[k] : row[k] >> 1)];
         }
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             if (base + k * FLAT_GROUPS >= total) continue;
             float x[8];
+            codes_trim<TINY>(c[k], (int)col[k], (int)d);
             block_decode(c[k], scale[k], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += shift[k];
@@ -149,17 +164,24 @@ __global__ __launch_bounds__(FLAT_BLOCK) void restore_kernel(
 }
 
 // KEPT: gate (and up) restored from the codes; else read from x.
-template <int DT, int ACT, bool KEPT, int UNROLL>
+template <int DT, int ACT, bool KEPT, bool TINY>
 __global__ __launch_bounds__(FLAT_BLOCK) void backward_kernel(
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, typename Elem<DT>::storage *__restrict__ dx,
     int32_t rows_cap, uint32_t d, uint32_t nb, FastDiv by_nb, const int32_t *__restrict__ live) {
     constexpr bool GATED = ACT != OP_SQUARED_RELU;
-    constexpr int H = GATED ? 2 : 1;
+    constexpr int H = GATED ? 2 : 1, UNROLL = unroll_of<DT>(H);
     const uint32_t rows = live != nullptr ? (uint32_t)clamp_live(live, rows_cap) : (uint32_t)rows_cap;
     const uint32_t total = rows * nb;
     const uint32_t step = gridDim.x * FLAT_GROUPS * UNROLL;
     const uint32_t l8 = (threadIdx.x & 15) * 8;
+    // a block's row and this lane's column; past the last block that one, unused
+    auto place = [&](uint32_t b, uint32_t &row, uint32_t &col, int &n) {
+        b = b < total ? b : total - 1;
+        row = by_nb(b);
+        col = (b - row * nb) * BLOCK8 + l8;
+        n = (int)d - (int)col;
+    };
     for (uint32_t base = blockIdx.x * FLAT_GROUPS * UNROLL + (threadIdx.x >> 4); base < total; base += step) {
         Oct<DT> dy[UNROLL], g[UNROLL], u[UNROLL];
         uint2 cg[UNROLL], cu[UNROLL];
@@ -169,33 +191,37 @@ __global__ __launch_bounds__(FLAT_BLOCK) void backward_kernel(
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             const uint32_t b = base + k * FLAT_GROUPS;
-            row[k] = by_nb(b < total ? b : 0);
-            col[k] = (b - row[k] * nb) * BLOCK8 + l8;
-            n[k] = (int)d - (int)col[k];
-            if (b < total) {
-                const size_t at = (size_t)row[k] * (H * d) + col[k];
-                oct_load<DT>(dy[k], dout + (size_t)row[k] * d + col[k], n[k]);
-                if constexpr (KEPT) {
-                    const size_t block = (size_t)row[k] * (H * nb) + (b - row[k] * nb);
-                    cg[k] = codes_load(codes + at, n[k]);
-                    sg[k] = scales[block];
-                    if constexpr (GATED) {
-                        cu[k] = codes_load(codes + at + d, n[k]);
-                        su[k] = scales[block + nb];
-                    }
-                } else {
-                    oct_load<DT>(g[k], in + at, n[k]);
-                    if constexpr (GATED) oct_load<DT>(u[k], in + at + d, n[k]);
+            place(b, row[k], col[k], n[k]);
+            oct_fetch<DT, TINY>(dy[k], dout + (size_t)row[k] * d, (int)col[k], (int)d);
+            const size_t at = (size_t)row[k] * (H * d);
+            if constexpr (KEPT) {
+                const size_t block = (size_t)row[k] * (H * nb) + col[k] / BLOCK8;
+                cg[k] = codes_fetch<TINY>(codes + at, (int)col[k], (int)d);
+                sg[k] = scales[block];
+                if constexpr (GATED) {
+                    cu[k] = codes_fetch<TINY>(codes + at + d, (int)col[k], (int)d);
+                    su[k] = scales[block + nb];
                 }
+            } else {
+                oct_fetch<DT, TINY>(g[k], in + at, (int)col[k], (int)d);
+                if constexpr (GATED) oct_fetch<DT, TINY>(u[k], in + at + d, (int)col[k], (int)d);
             }
         }
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             if (base + k * FLAT_GROUPS >= total) continue;
             float x[8], t[8], a[8], v[8];
+            oct_trim<DT, TINY>(dy[k], (int)col[k], (int)d);
             oct_unpack<DT>(dy[k], t);
-            if constexpr (KEPT) block_decode(cg[k], sg[k], x);
-            else oct_unpack<DT>(g[k], x);
+            if constexpr (KEPT) {
+                codes_trim<TINY>(cg[k], (int)col[k], (int)d);
+                if constexpr (GATED) codes_trim<TINY>(cu[k], (int)col[k], (int)d);
+                block_decode(cg[k], sg[k], x);
+            } else {
+                oct_trim<DT, TINY>(g[k], (int)col[k], (int)d);
+                if constexpr (GATED) oct_trim<DT, TINY>(u[k], (int)col[k], (int)d);
+                oct_unpack<DT>(g[k], x);
+            }
             const size_t at = (size_t)row[k] * (H * d) + col[k];
             if constexpr (GATED) {
                 float up[8];
@@ -219,18 +245,13 @@ __global__ __launch_bounds__(FLAT_BLOCK) void backward_kernel(
     }
 }
 
-constexpr int UNROLL16 = 2;  // 16-bit elements
-constexpr int UNROLL32 = 1;  // fp32: two loads an octet already
-
-template <int DT> constexpr int unroll_of() { return DT == DT_F32 ? UNROLL32 : UNROLL16; }
-
 // One workgroup per FLAT_GROUPS * unroll blocks; past GRID_MOST workgroups
 // the grid strides.
 constexpr int64_t GRID_MOST = 1 << 22;
 
 template <int DT>
-dim3 flat_grid(int64_t blocks) {
-    const int64_t per = FLAT_GROUPS * unroll_of<DT>();
+dim3 flat_grid(int64_t blocks, int halves) {
+    const int64_t per = FLAT_GROUPS * unroll_of<DT>(halves);
     const int64_t g = (blocks + per - 1) / per;
     return dim3((uint32_t)(g < GRID_MOST ? g : GRID_MOST));
 }
@@ -240,8 +261,10 @@ hipError_t store_as(const void *in, void *out, void *codes, float *scales, int32
                     const int32_t *live, hipStream_t stream) {
     using S = typename Elem<DT>::storage;
     const uint32_t nb = (d + BLOCK8 - 1) / BLOCK8;
-    store_kernel<DT, ACT, unroll_of<DT>()><<<flat_grid<DT>((int64_t)rows * nb), FLAT_BLOCK, 0, stream>>>(
-        (const S *)in, (S *)out, (uint8_t *)codes, scales, rows, d, nb, FastDiv(nb), live);
+    const dim3 grid = flat_grid<DT>((int64_t)rows * nb, ACT == OP_NONE || ACT == OP_SQUARED_RELU ? 1 : 2);
+    const auto kernel = d < 8 ? store_kernel<DT, ACT, true> : store_kernel<DT, ACT, false>;
+    kernel<<<grid, FLAT_BLOCK, 0, stream>>>((const S *)in, (S *)out, (uint8_t *)codes, scales, rows, d, nb, FastDiv(nb),
+                                            live);
     return hipGetLastError();
 }
 
@@ -262,7 +285,8 @@ template <int DT>
 hipError_t restore_as(const void *codes, const float *scales, const float *stats, void *out, int32_t rows, uint32_t d,
                       int32_t halves, const int32_t *live, hipStream_t stream) {
     const uint32_t nb = (d + BLOCK8 - 1) / BLOCK8;
-    restore_kernel<DT, unroll_of<DT>()><<<flat_grid<DT>((int64_t)rows * halves * nb), FLAT_BLOCK, 0, stream>>>(
+    const auto kernel = d < 8 ? restore_kernel<DT, true> : restore_kernel<DT, false>;
+    kernel<<<flat_grid<DT>((int64_t)rows * halves * nb, 1), FLAT_BLOCK, 0, stream>>>(
         (const uint8_t *)codes, scales, stats, (typename Elem<DT>::storage *)out, rows, d, nb, FastDiv(nb), halves,
         live);
     return hipGetLastError();
@@ -273,13 +297,11 @@ hipError_t backward_as(const void *dout, const void *in, const void *codes, cons
                        int32_t rows, uint32_t d, const int32_t *live, hipStream_t stream) {
     using S = typename Elem<DT>::storage;
     const uint32_t nb = (d + BLOCK8 - 1) / BLOCK8;
-    const dim3 grid = flat_grid<DT>((int64_t)rows * nb);
-    if (in != nullptr)
-        backward_kernel<DT, ACT, false, unroll_of<DT>()><<<grid, FLAT_BLOCK, 0, stream>>>(
-            (const S *)dout, (const S *)in, nullptr, nullptr, (S *)dx, rows, d, nb, FastDiv(nb), live);
-    else
-        backward_kernel<DT, ACT, true, unroll_of<DT>()><<<grid, FLAT_BLOCK, 0, stream>>>(
-            (const S *)dout, nullptr, (const uint8_t *)codes, scales, (S *)dx, rows, d, nb, FastDiv(nb), live);
+    const dim3 grid = flat_grid<DT>((int64_t)rows * nb, ACT == OP_SQUARED_RELU ? 1 : 2);
+    const auto kernel = in == nullptr ? (d < 8 ? backward_kernel<DT, ACT, true, true> : backward_kernel<DT, ACT, true, false>)
+                                      : (d < 8 ? backward_kernel<DT, ACT, false, true> : backward_kernel<DT, ACT, false, false>);
+    kernel<<<grid, FLAT_BLOCK, 0, stream>>>((const S *)dout, (const S *)in, (const uint8_t *)codes, scales, (S *)dx, rows,
+                                            d, nb, FastDiv(nb), live);
     return hipGetLastError();
 }
 

@@ -105,6 +105,16 @@ __device__ __forceinline__ void oct_store(typename Elem<DT>::storage *p, const f
     }
 }
 
+// Between two uses of the same raw octet: without it the compiler keeps the
+// first use's eight fp32 values for the second, twice the registers of a
+// 16-bit octet and four times those of codes.
+template <int DT>
+__device__ __forceinline__ void stay_raw(Oct<DT> &o) {
+#pragma unroll
+    for (int i = 0; i < Oct<DT>::WORDS; ++i) asm volatile("" : "+v"(o.w[i]));
+}
+__device__ __forceinline__ void stay_raw(uint2 &k) { asm volatile("" : "+v"(k.x), "+v"(k.y)); }
+
 // Eight codes of a checkpoint (two words, element e in byte e).
 __device__ __forceinline__ uint2 codes_load(const uint8_t *p, int n) {
     if (n >= 8) {

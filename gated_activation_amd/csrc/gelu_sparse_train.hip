@@ -61,6 +61,12 @@ __device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lan
     shifted_moments(s1, s2, (double)first, (double)d, mean, var);
 }
 
+template <int DT, int W, int V, bool TINY>
+__device__ __forceinline__ void trim_all(Oct<DT> (&o)[V], uint32_t lane, int d) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) oct_trim<DT, TINY>(o[v], (int)(v * 64 * W + lane) * 8, d);
+}
+
 // fp32(gate - cutoff) of an octet; 0 past the row's end.
 template <int DT>
 __device__ __forceinline__ void over_cutoff(const Oct<DT> &g, const RowOrigin<DT> &cutoff, int n, float (&t)[8]) {
@@ -73,11 +79,12 @@ __device__ __forceinline__ void over_cutoff(const Oct<DT> &g, const RowOrigin<DT
     }
 }
 
-// Waves a SIMD holds at least: 16-wave workgroups of two octets a lane pair up
-// on a compute unit within 64 registers (a third register pair halves that).
-template <int DT, int W, int V> constexpr int sparse_waves() { return DT != DT_F32 && W == 16 && V == 2 ? 8 : 4; }
+// Waves a SIMD holds at least.  16-wave workgroups pair up on a compute unit
+// within 64 registers, which two octets a lane of 16-bit values fit.
+template <int DT, int W, int V> constexpr int sparse_waves() { return DT == DT_F32 || V > 2 ? 4 : W == 16 ? 8 : 6; }
 
-template <int DT, int W, int V>
+// TINY: rows of fewer than eight values.
+template <int DT, int W, int V, bool TINY>
 __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void sparse_store_kernel(
     const typename Elem<DT>::storage *__restrict__ in, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
@@ -87,21 +94,20 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
     if (at.row >= live_rows) return;
     const typename Elem<DT>::storage *x = in + (size_t)at.row * 2 * d;
-    Oct<DT> g[V];
+    Oct<DT> g[V], u[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * 64 * W + at.lane) * 8;
-        oct_load<DT>(g[v], x + c, d - c);
-    }
-    Oct<DT> u[V];
+    for (int v = 0; v < V; ++v) oct_fetch<DT, TINY>(g[v], x, (int)(v * 64 * W + at.lane) * 8, d);
+    constexpr bool EARLY = V <= 4;  // up with the gate, while registers last
+    if constexpr (EARLY) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * 64 * W + at.lane) * 8;
-        oct_load<DT>(u[v], x + d + c, d - c);
+        for (int v = 0; v < V; ++v) oct_fetch<DT, TINY>(u[v], x + d, (int)(v * 64 * W + at.lane) * 8, d);
     }
     const float first = Elem<DT>::to_f32(x[0]);
     double mean, var;
+    trim_all<DT, W, V, TINY>(g, at.lane, d);
     gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
+#pragma unroll
+    for (int v = 0; v < V; ++v) stay_raw(g[v]);
     const double std = __builtin_sqrt(var);
     const RowOrigin<DT> cutoff(__builtin_fma((double)z, std, mean));
     if (at.lane == 0) {
@@ -115,12 +121,17 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         const int c = (int)(v * 64 * W + at.lane) * 8;
         const int n = d - c;
         const uint32_t block = (uint32_t)c / BLOCK8;
+        if constexpr (!EARLY) {
+            __builtin_amdgcn_sched_barrier(0);
+            oct_fetch<DT, TINY>(u[v], x + d, c, d);
+        }
         if (block >= nb) continue;  // the same for the 16 lanes of a block
         float t[8], up[8], scale;
         over_cutoff<DT>(g[v], cutoff, n, t);
         const uint2 ct = block_encode<difference_of<DT>(), true>(t, scale);
         codes_store(row_codes + c, ct, n);
         if ((at.lane & 15) == 0) row_scales[block] = scale;
+        oct_trim<DT, TINY>(u[v], c, d);
         oct_unpack<DT>(u[v], up);
         const uint2 cu = block_encode<code_of<DT>(), false>(up, scale);
         codes_store(row_codes + d + c, cu, n);
@@ -132,8 +143,8 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
 }
 
 // KEPT: t and up restored from the codes, s from stats; else from x.
-template <int DT, int W, int V, bool KEPT>
-__global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
+template <int DT, int W, int V, bool TINY, bool KEPT>
+__global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void sparse_backward_kernel(
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const float *__restrict__ stats,
     typename Elem<DT>::storage *__restrict__ dx, int32_t rows, int32_t d, uint32_t nb, float z,
@@ -145,23 +156,47 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
     if (at.row >= live_rows) return;
     const size_t row2 = (size_t)at.row * 2 * d;
     const typename Elem<DT>::storage *dy = dout + (size_t)at.row * d;
-    Oct<DT> g[KEPT ? 1 : V];
-    uint2 ct[KEPT ? V : 1];
-    float st[KEPT ? V : 1];
+    // all of the row's loads at once with up to two octets a lane
+    constexpr bool EARLY = V <= 2;
+    Oct<DT> g[KEPT ? 1 : V], o[V], u[KEPT ? 1 : V];
+    uint2 ct[KEPT ? V : 1], cu[KEPT ? V : 1];
+    float st[KEPT ? V : 1], su[KEPT ? V : 1];
+    auto load = [&](int v) {
+        const int c = (int)(v * 64 * W + at.lane) * 8;
+        oct_fetch<DT, TINY>(o[v], dy, c, d);
+        if constexpr (KEPT) {
+            const uint32_t block = (uint32_t)c / BLOCK8 < nb ? (uint32_t)c / BLOCK8 : nb - 1;
+            const float *row_scales = scales + (size_t)at.row * 2 * nb + block;
+            ct[v] = codes_fetch<TINY>(codes + row2, c, d);
+            cu[v] = codes_fetch<TINY>(codes + row2 + d, c, d);
+            st[v] = row_scales[0];
+            su[v] = row_scales[nb];
+        } else {
+            oct_fetch<DT, TINY>(u[v], in + row2 + d, c, d);
+        }
+    };
     RowOrigin<DT> cutoff(0.0);
     float s;
     if constexpr (KEPT) {
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) load(v);
+        }
         s = stats[2 * (size_t)at.row + 1];
     } else {
         const typename Elem<DT>::storage *x = in + row2;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (int)(v * 64 * W + at.lane) * 8;
-            oct_load<DT>(g[v], x + c, d - c);
-        }
+        for (int v = 0; v < V; ++v) oct_fetch<DT, TINY>(g[v], x, (int)(v * 64 * W + at.lane) * 8, d);
         const float first = Elem<DT>::to_f32(x[0]);
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) load(v);
+        }
         double mean, var;
+        trim_all<DT, W, V, TINY>(g, at.lane, d);
         gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
+#pragma unroll
+        for (int v = 0; v < V; ++v) stay_raw(g[v]);
         const double std = __builtin_sqrt(var);
         cutoff = RowOrigin<DT>(__builtin_fma((double)z, std, mean));
         s = (float)std;
@@ -171,36 +206,36 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * 64 * W + at.lane) * 8;
         const int n = d - c;
-        if (n <= 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[v][e] = 0.0f;
-            continue;
-        }
-        Oct<DT> o;
         float t[8], up[8], dv[8], du[8];
-        oct_load<DT>(o, dy + c, n);
+        if constexpr (V > 2) __builtin_amdgcn_sched_barrier(0);  // one octet at a time: interleaved they spill
+        if constexpr (!EARLY) load(v);
+        oct_trim<DT, TINY>(o[v], c, d);
         if constexpr (KEPT) {
-            const float *row_scales = scales + (size_t)at.row * 2 * nb + (uint32_t)c / BLOCK8;
-            ct[v] = codes_load(codes + row2 + c, n);
-            st[v] = row_scales[0];
+            codes_trim<TINY>(ct[v], c, d);
+            codes_trim<TINY>(cu[v], c, d);
             block_decode(ct[v], st[v], t);
-            block_decode(codes_load(codes + row2 + d + c, n), row_scales[nb], up);
+            block_decode(cu[v], su[v], up);
         } else {
-            Oct<DT> u;
-            oct_load<DT>(u, in + row2 + d + c, n);
+            oct_trim<DT, TINY>(u[v], c, d);
             over_cutoff<DT>(g[v], cutoff, n, t);
-            oct_unpack<DT>(u, up);
+            oct_unpack<DT>(u[v], up);
         }
-        oct_unpack<DT>(o, dv);
+        oct_unpack<DT>(o[v], dv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float f, df;
             gelu_tanh_slope(__builtin_fmaxf(t[e], 0.0f), f, df);
             q[v][e] = t[e] > 0.0f ? dv[e] * up[e] * df : 0.0f;
+            asm volatile("" : "+v"(q[v][e]));  // else its factors are kept for a later fma: twice the registers
             du[e] = dv[e] * f;
             total += q[v][e];
         }
         oct_store<DT>(dx + row2 + d + c, du, n);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if constexpr (KEPT) stay_raw(ct[v]);
+        else stay_raw(g[v]);
     }
     float unused = 0.0f;
     team_sum2<64 * W>(total, unused, sums);
@@ -211,6 +246,7 @@ __global__ __launch_bounds__(team_block<W>()) void sparse_backward_kernel(
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * 64 * W + at.lane) * 8;
         const int n = d - c;
+        if constexpr (V > 2) __builtin_amdgcn_sched_barrier(0);
         if (n <= 0) continue;
         float t[8];
         if constexpr (KEPT) block_decode(ct[v], st[v], t);
@@ -234,46 +270,48 @@ struct Args {
 
 enum Pass { STORE, BACKWARD, BACKWARD_KEPT };
 
-template <int DT, int W, int V>
-hipError_t launch_as(Pass pass, const Args &a) {
+template <Pass P, int DT, int W, int V, bool TINY = false>
+hipError_t launch_as(const Args &a) {
     using S = typename Elem<DT>::storage;
     const uint32_t nb = ((uint32_t)a.d + BLOCK8 - 1) / BLOCK8;
     const dim3 grid((uint32_t)(((int64_t)a.rows + team_rows<W>() - 1) / team_rows<W>()));
     const dim3 block(team_block<W>());
-    if (pass == STORE)
-        sparse_store_kernel<DT, W, V><<<grid, block, 0, a.stream>>>((const S *)a.in, (S *)a.out, (uint8_t *)a.codes,
-                                                                    a.scales, a.stats, a.rows, a.d, nb, a.z, a.live);
-    else if (pass == BACKWARD)
-        sparse_backward_kernel<DT, W, V, false><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, (const S *)a.in, nullptr, nullptr, nullptr, (S *)a.out, a.rows, a.d, nb, a.z, a.live);
+    if constexpr (P == STORE)
+        sparse_store_kernel<DT, W, V, TINY><<<grid, block, 0, a.stream>>>(
+            (const S *)a.in, (S *)a.out, (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, nb, a.z, a.live);
     else
-        sparse_backward_kernel<DT, W, V, true><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, nullptr, (const uint8_t *)a.codes, a.scales, a.stats, (S *)a.out, a.rows, a.d, nb, a.z,
-            a.live);
+        sparse_backward_kernel<DT, W, V, TINY, P == BACKWARD_KEPT><<<grid, block, 0, a.stream>>>(
+            (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats, (S *)a.out, a.rows, a.d, nb,
+            a.z, a.live);
     return hipGetLastError();
 }
 
-template <int DT>
-hipError_t launch_dt(Pass pass, const Args &a) {
-    const int waves = sparse_train_waves(a.d);
-    const int64_t octets = ((int64_t)a.d + 7) / 8;
-    const int64_t v = (octets + 64 * waves - 1) / (64 * waves);
-    switch (waves) {
-    case 1: return v <= 1 ? launch_as<DT, 1, 1>(pass, a) : launch_as<DT, 1, 2>(pass, a);
-    case 2: return launch_as<DT, 2, 2>(pass, a);
-    case 4: return launch_as<DT, 4, 2>(pass, a);
-    case 8: return launch_as<DT, 8, 2>(pass, a);
-    default:
-        return v <= 2 ? launch_as<DT, 16, 2>(pass, a) : v <= 4 ? launch_as<DT, 16, 4>(pass, a)
-                                                               : launch_as<DT, 16, 8>(pass, a);
+template <Pass P, int DT>
+hipError_t launch_dt(const Args &a) {
+    if (a.d < 8) return launch_as<P, DT, 1, 1, true>(a);
+    if (a.d <= 512) return launch_as<P, DT, 1, 1>(a);
+    switch (sparse_train_waves(a.d)) {
+    case 1: return launch_as<P, DT, 1, 2>(a);
+    case 2: return launch_as<P, DT, 2, 2>(a);
+    case 4: return launch_as<P, DT, 4, 2>(a);
+    case 8: return launch_as<P, DT, 8, 2>(a);
+    default: break;
     }
+    // From x at 16 waves of two octets the backward needs more than the 64
+    // registers that let two workgroups share a compute unit: 2048 rows of
+    // 16384, bf16, 69 us, against 59 us for eight waves of four.
+    constexpr int W = P == BACKWARD ? 8 : 16;
+    if (a.d <= 16384) return launch_as<P, DT, W, 32 / W>(a);
+    if (a.d <= 32768) return launch_as<P, DT, 16, 4>(a);
+    return launch_as<P, DT, 16, 8>(a);
 }
 
-hipError_t launch_any(int dtype, Pass pass, const Args &a) {
+template <Pass P>
+hipError_t launch_pass(int dtype, const Args &a) {
     switch (dtype) {
-    case DT_F32: return launch_dt<DT_F32>(pass, a);
-    case DT_F16: return launch_dt<DT_F16>(pass, a);
-    case DT_BF16: return launch_dt<DT_BF16>(pass, a);
+    case DT_F32: return launch_dt<P, DT_F32>(a);
+    case DT_F16: return launch_dt<P, DT_F16>(a);
+    case DT_BF16: return launch_dt<P, DT_BF16>(a);
     default: return hipErrorInvalidValue;
     }
 }
@@ -289,15 +327,15 @@ int sparse_train_waves(int64_t d) {
 
 hipError_t launch_sparse_store(int dtype, const void *in, void *out, void *codes, float *scales, float *stats,
                                int32_t rows, int32_t d, float z, const int32_t *live, hipStream_t stream) {
-    return launch_any(dtype, STORE, Args{nullptr, in, out, codes, scales, stats, rows, d, z, live, stream});
+    return launch_pass<STORE>(dtype, Args{nullptr, in, out, codes, scales, stats, rows, d, z, live, stream});
 }
 
 hipError_t launch_sparse_backward(int dtype, const void *dout, const void *in, const void *codes, const float *scales,
                                   const float *stats, void *dx, int32_t rows, int32_t d, float z, const int32_t *live,
                                   hipStream_t stream) {
-    return launch_any(dtype, in != nullptr ? BACKWARD : BACKWARD_KEPT,
-                      Args{dout, in, dx, const_cast<void *>(codes), const_cast<float *>(scales),
-                           const_cast<float *>(stats), rows, d, z, live, stream});
+    const Args a{dout, in, dx, const_cast<void *>(codes), const_cast<float *>(scales), const_cast<float *>(stats),
+                 rows, d, z, live, stream};
+    return in != nullptr ? launch_pass<BACKWARD>(dtype, a) : launch_pass<BACKWARD_KEPT>(dtype, a);
 }
 
 }  // namespace ga
