@@ -263,9 +263,8 @@ hipError_t store_as(const void *in, void *out, void *codes, float *scales, int32
     const uint32_t nb = (d + BLOCK8 - 1) / BLOCK8;
     const dim3 grid = flat_grid<DT>((int64_t)rows * nb, ACT == OP_NONE || ACT == OP_SQUARED_RELU ? 1 : 2);
     const auto kernel = d < 8 ? store_kernel<DT, ACT, true> : store_kernel<DT, ACT, false>;
-    kernel<<<grid, FLAT_BLOCK, 0, stream>>>((const S *)in, (S *)out, (uint8_t *)codes, scales, rows, d, nb, FastDiv(nb),
-                                            live);
-    return hipGetLastError();
+    return launch_kernel(kernel, grid, FLAT_BLOCK, stream, (const S *)in, (S *)out, (uint8_t *)codes, scales, rows, d, nb,
+                         FastDiv(nb), live);
 }
 
 template <int DT>
@@ -286,10 +285,9 @@ hipError_t restore_as(const void *codes, const float *scales, const float *stats
                       int32_t halves, const int32_t *live, hipStream_t stream) {
     const uint32_t nb = (d + BLOCK8 - 1) / BLOCK8;
     const auto kernel = d < 8 ? restore_kernel<DT, true> : restore_kernel<DT, false>;
-    kernel<<<flat_grid<DT>((int64_t)rows * halves * nb, 1), FLAT_BLOCK, 0, stream>>>(
-        (const uint8_t *)codes, scales, stats, (typename Elem<DT>::storage *)out, rows, d, nb, FastDiv(nb), halves,
-        live);
-    return hipGetLastError();
+    return launch_kernel(kernel, flat_grid<DT>((int64_t)rows * halves * nb, 1), FLAT_BLOCK, stream,
+                         (const uint8_t *)codes, scales, stats, (typename Elem<DT>::storage *)out, rows, d, nb,
+                         FastDiv(nb), halves, live);
 }
 
 template <int DT, int ACT>
@@ -300,9 +298,8 @@ hipError_t backward_as(const void *dout, const void *in, const void *codes, cons
     const dim3 grid = flat_grid<DT>((int64_t)rows * nb, ACT == OP_SQUARED_RELU ? 1 : 2);
     const auto kernel = in == nullptr ? (d < 8 ? backward_kernel<DT, ACT, true, true> : backward_kernel<DT, ACT, true, false>)
                                       : (d < 8 ? backward_kernel<DT, ACT, false, true> : backward_kernel<DT, ACT, false, false>);
-    kernel<<<grid, FLAT_BLOCK, 0, stream>>>((const S *)dout, (const S *)in, (const uint8_t *)codes, scales, (S *)dx, rows,
-                                            d, nb, FastDiv(nb), live);
-    return hipGetLastError();
+    return launch_kernel(kernel, grid, FLAT_BLOCK, stream, (const S *)dout, (const S *)in, (const uint8_t *)codes, scales,
+                         (S *)dx, rows, d, nb, FastDiv(nb), live);
 }
 
 template <int DT>

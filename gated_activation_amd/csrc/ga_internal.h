@@ -7,7 +7,18 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace ga {
+
+// Enqueues kernel(args...), each argument converted to the kernel's own
+// parameter type, and returns this launch's status.
+template <typename... P>
+hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream,
+                         typename std::common_type<P>::type... args) {
+    void *pointers[] = {(void *)&args...};
+    return hipLaunchKernel((const void *)kernel, grid, block, pointers, 0, stream);
+}
 
 // Geometries with a compiled kernel.
 bool gelu_vec_available(int dtype, int waves, int vec_per_lane, int up_late);

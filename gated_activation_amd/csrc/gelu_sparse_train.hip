@@ -277,13 +277,12 @@ hipError_t launch_as(const Args &a) {
     const dim3 grid((uint32_t)(((int64_t)a.rows + team_rows<W>() - 1) / team_rows<W>()));
     const dim3 block(team_block<W>());
     if constexpr (P == STORE)
-        sparse_store_kernel<DT, W, V, TINY><<<grid, block, 0, a.stream>>>(
-            (const S *)a.in, (S *)a.out, (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, nb, a.z, a.live);
+        return launch_kernel(sparse_store_kernel<DT, W, V, TINY>, grid, block, a.stream, (const S *)a.in, (S *)a.out,
+                             (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, nb, a.z, a.live);
     else
-        sparse_backward_kernel<DT, W, V, TINY, P == BACKWARD_KEPT><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats, (S *)a.out, a.rows, a.d, nb,
-            a.z, a.live);
-    return hipGetLastError();
+        return launch_kernel(sparse_backward_kernel<DT, W, V, TINY, P == BACKWARD_KEPT>, grid, block, a.stream,
+                             (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats,
+                             (S *)a.out, a.rows, a.d, nb, a.z, a.live);
 }
 
 template <Pass P, int DT>

@@ -450,15 +450,9 @@ hipError_t forward_as(const Forward &a) {
     using WS = typename Elem<weight_type<DT, WIDE>()>::storage;
     constexpr int BLOCK = forward_block<T::LANES>(), TEAMS = BLOCK / T::LANES;
     const dim3 grid((uint32_t)(((int64_t)a.rows + TEAMS - 1) / TEAMS)), block(BLOCK);
-    if (a.codes != nullptr)
-        forward_kernel<DT, WIDE, T, true><<<grid, block, 0, a.stream>>>(
-            (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias, (S *)a.out, (uint8_t *)a.codes, a.scales,
-            a.stats, a.rows, a.d, a.eps, a.live);
-    else
-        forward_kernel<DT, WIDE, T, false><<<grid, block, 0, a.stream>>>(
-            (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias, (S *)a.out, nullptr, nullptr, a.stats, a.rows,
-            a.d, a.eps, a.live);
-    return hipGetLastError();
+    const auto kernel = a.codes != nullptr ? forward_kernel<DT, WIDE, T, true> : forward_kernel<DT, WIDE, T, false>;
+    return launch_kernel(kernel, grid, block, a.stream, (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias,
+                         (S *)a.out, (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, a.eps, a.live);
 }
 
 template <int DT, bool WIDE>
@@ -490,28 +484,25 @@ hipError_t backward_as(const Backward &a) {
     const dim3 grid((uint32_t)(a.groups * strips)), block(BACK_BLOCK);
     auto launch = [&](auto kept, auto stage) {
         constexpr bool KEPT = decltype(kept)::value;
-        backward_kernel<DT, WIDE, T, KEPT, decltype(stage)::value><<<grid, block, 0, a.stream>>>(
-            (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats, (const WS *)a.weight,
-            (S *)a.dx, (WS *)a.dweight, (WS *)a.dbias, partial, row_sums, a.rows, a.d, a.live);
+        return launch_kernel(backward_kernel<DT, WIDE, T, KEPT, decltype(stage)::value>, grid, block, a.stream,
+                             (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats,
+                             (const WS *)a.weight, (S *)a.dx, (WS *)a.dweight, (WS *)a.dbias, partial, row_sums, a.rows,
+                             a.d, a.live);
     };
     auto launches = [&](auto kept) {
         if constexpr (T::LANES == BACK_BLOCK) {
             if (strips > 1) {
-                launch(kept, std::integral_constant<Stage, SUMS>());
-                launch(kept, std::integral_constant<Stage, APPLY>());
-                return;
+                const hipError_t e = launch(kept, std::integral_constant<Stage, SUMS>());
+                return e != hipSuccess ? e : launch(kept, std::integral_constant<Stage, APPLY>());
             }
         }
-        launch(kept, std::integral_constant<Stage, WHOLE>());
+        return launch(kept, std::integral_constant<Stage, WHOLE>());
     };
-    if (a.kept) launches(std::true_type());
-    else launches(std::false_type());
-    hipError_t e = hipGetLastError();
+    const hipError_t e = a.kept ? launches(std::true_type()) : launches(std::false_type());
     if (e != hipSuccess || a.groups == 1) return e;
-    reduce_kernel<WT><<<dim3((uint32_t)((2 * a.d + REDUCE_COLS - 1) / REDUCE_COLS)),
-                        dim3(REDUCE_COLS * REDUCE_SLICES), 0, a.stream>>>(partial, (WS *)a.dweight, (WS *)a.dbias,
-                                                                          a.groups, a.d);
-    return hipGetLastError();
+    return launch_kernel(reduce_kernel<WT>, dim3((uint32_t)((2 * a.d + REDUCE_COLS - 1) / REDUCE_COLS)),
+                         dim3(REDUCE_COLS * REDUCE_SLICES), a.stream, partial, (WS *)a.dweight, (WS *)a.dbias, a.groups,
+                         a.d);
 }
 
 template <int DT, bool WIDE>
