@@ -166,7 +166,7 @@ hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *w
 // of the weight's and the bias' gradient in the workspace ([groups, 2, d] fp32;
 // none with one group), after two sums for each strip of rows that are cut into
 // strips.  kept: from codes and scales, else from in.
-int layer_norm_groups(int64_t rows, int64_t d, int cus);
+int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus);
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups);
 hipError_t launch_layer_norm_backward(int dtype, bool wide, const void *dout, const void *in, const void *codes,
                                       const float *scales, const float *stats, const void *weight, void *dx,

@@ -160,7 +160,7 @@ ga_status layer_norm_backward(const char *op, const void *dout, const void *in, 
     return ga::launched(op, ga::launch_layer_norm_backward(
                                 dtype, weight_dtype == GA_F32, dout, kept ? nullptr : in, kept ? codes : nullptr, scales,
                                 stats, weight, dx, dweight, dbias, kept, (int32_t)rows, (int32_t)d, live_rows,
-                                ga::layer_norm_groups(rows, d, cus), (float *)workspace, (hipStream_t)stream));
+                                ga::layer_norm_groups(rows, d, dtype == GA_F32, cus), (float *)workspace, (hipStream_t)stream));
 }
 
 ga_status check_balance(const char *op, int64_t rows, int64_t experts, int64_t k, int32_t dtype, float coefficient) {
@@ -305,7 +305,8 @@ ga_status ga_layer_norm_checkpoint(const void *in, const void *weight, const voi
 
 size_t ga_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
     if (rows < 1 || rows > INT32_MAX || d < 1 || d > ga::LN_MAX_D) return 0;
-    return ga::layer_norm_workspace_bytes(rows, d, ga::layer_norm_groups(rows, d, kMostCus));
+    // of any row type: 16-bit rows have more teams to a workgroup, so fp32 rows the more groups
+    return ga::layer_norm_workspace_bytes(rows, d, ga::layer_norm_groups(rows, d, true, kMostCus));
 }
 
 ga_status ga_layer_norm_backward(const void *dout, const void *in, const float *stats, const void *weight, void *dx,
