@@ -214,6 +214,8 @@ def activation_backward(dout, kept, activation, z=Z_SPARSITY_095, live_rows=None
         _like(kept, (rows, halves * d), dtype, device, "x", name)
     else:
         _given(kept, sparse, name)
+        if not sparse and kept.stats is not None:
+            raise ValueError(f"{name}: the Checkpoint's codes are relative to their rows (it has stats): not of {activation}")
         kept = _checkpoint(kept, rows, halves, d, sparse, device, name)
     out = _like(out, (rows, halves * d), dtype, device, "out", name)
     live = _live(live_rows, device, name)

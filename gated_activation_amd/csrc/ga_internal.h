@@ -159,9 +159,11 @@ hipError_t launch_sparse_backward(int dtype, const void *dout, const void *in, c
 // Layer norm, d <= LN_MAX_D.  wide: weight, bias and their gradients are fp32,
 // else of `dtype`.  With codes, the forward also keeps fp32(x - mean) there.
 constexpr int64_t LN_MAX_D = 32768;
+// The forward's launch has layer_norm_lanes(d) work-items a row.
+int layer_norm_lanes(int64_t d);
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
                              void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
-                             const int32_t *live, int cus, hipStream_t stream);
+                             const int32_t *live, hipStream_t stream);
 // Groups of rows in the backward's launch, each of which leaves one partial row
 // of the weight's and the bias' gradient in the workspace ([groups, 2, d] fp32;
 // none with one group), after two sums for each strip of rows that are cut into

@@ -150,8 +150,8 @@ __device__ __forceinline__ void codes_store(uint8_t *p, uint2 c, int n) {
 // ---------------------------------------------------------------------------
 template <int DT, bool TINY, bool NT = true>
 __device__ __forceinline__ void oct_fetch(Oct<DT> &o, const typename Elem<DT>::storage *row, int c, int d) {
-    if constexpr (TINY) oct_load<DT, NT>(o, row + c, d - c);
-    else oct_load<DT, NT>(o, row + (c < d - 8 ? c : d - 8), 8);
+    if constexpr (TINY) oct_load<DT, NT>(o, row + (uint32_t)c, d - c);
+    else oct_load<DT, NT>(o, row + (uint32_t)(c < d - 8 ? c : d - 8), 8);
 }
 
 // Words i take words i + K where `on`, and 0 past the last.
@@ -189,8 +189,8 @@ __device__ __forceinline__ void oct_trim(Oct<DT> &o, int c, int d) {
 
 template <bool TINY>
 __device__ __forceinline__ uint2 codes_fetch(const uint8_t *row, int c, int d) {
-    if constexpr (TINY) return codes_load(row + c, d - c);
-    else return codes_load(row + (c < d - 8 ? c : d - 8), 8);
+    if constexpr (TINY) return codes_load(row + (uint32_t)c, d - c);
+    else return codes_load(row + (uint32_t)(c < d - 8 ? c : d - 8), 8);
 }
 
 template <bool TINY>
@@ -378,6 +378,13 @@ __device__ __forceinline__ double wave_sum(double v) {
     return (read_lane64(v, 0) + read_lane64(v, 16)) + (read_lane64(v, 32) + read_lane64(v, 48));
 }
 
+// A team's row as a scalar where a team is one wavefront or more.
+template <int LANES>
+__device__ __forceinline__ uint32_t team_row(uint32_t row) {
+    if constexpr (LANES >= 64) return (uint32_t)__builtin_amdgcn_readfirstlane((int)row);
+    else return row;
+}
+
 // Sums of two values over the team that shares a row: 16 lanes, a wavefront,
 // or LANES / 64 wavefronts of a workgroup (all of whose teams call it together).
 // `slots`: LDS of the team's own, 2 * LANES / 64 values that nothing else
@@ -451,9 +458,9 @@ template <int DT> struct RowOrigin {
 // of one repeated value has variance 0 exactly.  In fp64 the differences of
 // fp32 values are exact or carry 2^-53, and the subtraction loses at most
 // (mean - x0)^2 / var <= d <= 2^16 times that.
-__device__ __forceinline__ void shifted_moments(double s1, double s2, double x0, double d, double &mean, double &var) {
-    const double m = s1 / d;
-    const double v = s2 / d - m * m;
+__device__ __forceinline__ void shifted_moments(double s1, double s2, double x0, double inv_d, double &mean, double &var) {
+    const double m = s1 * inv_d;
+    const double v = s2 * inv_d - m * m;
     mean = x0 + m;
     var = v > 0.0 ? v : (v == v ? 0.0 : v);  // a NaN stays one
 }

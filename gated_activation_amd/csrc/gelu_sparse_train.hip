@@ -37,14 +37,14 @@ struct RowAt {
 
 template <int W>
 __device__ __forceinline__ RowAt row_of_team() {
-    if constexpr (W == 1) return {blockIdx.x * 4 + (threadIdx.x >> 6), threadIdx.x & 63};
+    if constexpr (W == 1) return {team_row<64>(blockIdx.x * 4 + (threadIdx.x >> 6)), threadIdx.x & 63};
     else return {blockIdx.x, threadIdx.x};
 }
 
 // Statistics of the row's gate octets; every lane of the team gets the same.
 template <int DT, int W, int V>
-__device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lane, int d, float first, double *slots,
-                                             double &mean, double &var) {
+__device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lane, int d, double inv_d, float first,
+                                             double *slots, double &mean, double &var) {
     double s1 = 0.0, s2 = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -58,7 +58,7 @@ __device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lan
         add_shifted<DT>(x, first, s1, s2);
     }
     team_sum2<64 * W>(s1, s2, slots);
-    shifted_moments(s1, s2, (double)first, (double)d, mean, var);
+    shifted_moments(s1, s2, (double)first, inv_d, mean, var);
 }
 
 template <int DT, int W, int V, bool TINY>
@@ -88,7 +88,7 @@ template <int DT, int W, int V, bool TINY>
 __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void sparse_store_kernel(
     const typename Elem<DT>::storage *__restrict__ in, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
-    uint32_t nb, float z, const int32_t *__restrict__ live) {
+    uint32_t nb, float z, double inv_d, const int32_t *__restrict__ live) {
     __shared__ double slots[2 * W];
     const RowAt at = row_of_team<W>();
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     const float first = Elem<DT>::to_f32(x[0]);
     double mean, var;
     trim_all<DT, W, V, TINY>(g, at.lane, d);
-    gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
+    gate_moments<DT, W, V>(g, at.lane, d, inv_d, first, slots, mean, var);
 #pragma unroll
     for (int v = 0; v < V; ++v) stay_raw(g[v]);
     const double std = __builtin_sqrt(var);
@@ -129,16 +129,16 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         float t[8], up[8], scale;
         over_cutoff<DT>(g[v], cutoff, n, t);
         const uint2 ct = block_encode<difference_of<DT>(), true>(t, scale);
-        codes_store(row_codes + c, ct, n);
+        codes_store(row_codes + (uint32_t)c, ct, n);
         if ((at.lane & 15) == 0) row_scales[block] = scale;
         oct_trim<DT, TINY>(u[v], c, d);
         oct_unpack<DT>(u[v], up);
         const uint2 cu = block_encode<code_of<DT>(), false>(up, scale);
-        codes_store(row_codes + d + c, cu, n);
+        codes_store(row_codes + (uint32_t)(d + c), cu, n);
         if ((at.lane & 15) == 0) row_scales[nb + block] = scale;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = gelu_tanh(__builtin_fmaxf(t[e], 0.0f)) * up[e];
-        oct_store<DT>(out + (size_t)at.row * d + c, t, n);
+        oct_store<DT>(out + (size_t)at.row * d + (uint32_t)c, t, n);
     }
 }
 
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const float *__restrict__ stats,
     typename Elem<DT>::storage *__restrict__ dx, int32_t rows, int32_t d, uint32_t nb, float z,
-    const int32_t *__restrict__ live) {
+    double inv_d, const int32_t *__restrict__ live) {
     __shared__ double slots[2 * W];
     __shared__ float sums[2 * W];
     const RowAt at = row_of_team<W>();
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         }
         double mean, var;
         trim_all<DT, W, V, TINY>(g, at.lane, d);
-        gate_moments<DT, W, V>(g, at.lane, d, first, slots, mean, var);
+        gate_moments<DT, W, V>(g, at.lane, d, inv_d, first, slots, mean, var);
 #pragma unroll
         for (int v = 0; v < V; ++v) stay_raw(g[v]);
         const double std = __builtin_sqrt(var);
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
             du[e] = dv[e] * f;
             total += q[v][e];
         }
-        oct_store<DT>(dx + row2 + d + c, du, n);
+        oct_store<DT>(dx + row2 + (uint32_t)(d + c), du, n);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     }
     float unused = 0.0f;
     team_sum2<64 * W>(total, unused, sums);
-    const float share = total / (float)d;
+    const float share = total * (float)inv_d;
     const float b = s == 0.0f ? 0.0f : share * z / s;
     const float a = s == 0.0f ? share : __builtin_fmaf(share, z * z, share);
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         else over_cutoff<DT>(g[v], cutoff, n, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = q[v][e] - __builtin_fmaf(b, t[e], a);
-        oct_store<DT>(dx + row2 + c, t, n);
+        oct_store<DT>(dx + row2 + (uint32_t)c, t, n);
     }
 }
 
@@ -276,13 +276,14 @@ hipError_t launch_as(const Args &a) {
     const uint32_t nb = ((uint32_t)a.d + BLOCK8 - 1) / BLOCK8;
     const dim3 grid((uint32_t)(((int64_t)a.rows + team_rows<W>() - 1) / team_rows<W>()));
     const dim3 block(team_block<W>());
+    const double inv_d = 1.0 / a.d;
     if constexpr (P == STORE)
         return launch_kernel(sparse_store_kernel<DT, W, V, TINY>, grid, block, a.stream, (const S *)a.in, (S *)a.out,
-                             (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, nb, a.z, a.live);
+                             (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, nb, a.z, inv_d, a.live);
     else
         return launch_kernel(sparse_backward_kernel<DT, W, V, TINY, P == BACKWARD_KEPT>, grid, block, a.stream,
                              (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats,
-                             (S *)a.out, a.rows, a.d, nb, a.z, a.live);
+                             (S *)a.out, a.rows, a.d, nb, a.z, inv_d, a.live);
 }
 
 template <Pass P, int DT>

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight,
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ bias, typename Elem<DT>::storage *__restrict__ out,
     uint8_t *__restrict__ codes, float *__restrict__ scales, float *__restrict__ stats, int32_t rows, int32_t d,
-    float eps, const int32_t *__restrict__ live) {
+    float eps, double inv_d, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
     constexpr int LANES = T::LANES, V = T::V;
     constexpr bool TINY = T::TINY;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
     const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
     if (blockIdx.x * TEAMS >= live_rows) return;
     const bool mine = blockIdx.x * TEAMS + team < live_rows;  // a team without a row follows the last one
-    const uint32_t row = mine ? blockIdx.x * TEAMS + team : live_rows - 1;
+    const uint32_t row = team_row<LANES>(mine ? blockIdx.x * TEAMS + team : live_rows - 1);
     const typename Elem<DT>::storage *x = in + (size_t)row * d;
     Oct<DT> o[V];
     Oct<WT> w[V], b[V];
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
     team_sum2<LANES>(s1, s2, slots[team]);
     if (!mine) return;
     double m, var;
-    shifted_moments(s1, s2, (double)first, (double)d, m, var);
+    shifted_moments(s1, s2, (double)first, inv_d, m, var);
     const RowOrigin<DT> mean(m);
     const float rstd = (float)(1.0 / __builtin_sqrt(var + (double)eps));
     if (lane == 0) {
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
             }
             float scale;
             const uint2 k = block_encode<difference_of<DT>(), false>(f, scale);
-            codes_store(codes + (size_t)row * d + c, k, n);
+            codes_store(codes + (size_t)row * d + (uint32_t)c, k, n);
             if ((lane & 15) == 0) scales[(size_t)row * nb + block] = scale;
         }
         oct_trim<WT, TINY>(w[v], c, d);
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, wf[e], bf[e]);
-        oct_store<DT>(out + (size_t)row * d + c, f, n);
+        oct_store<DT>(out + (size_t)row * d + (uint32_t)c, f, n);
     }
 }
 
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
         for (int e = 0; e < 8; ++e) aw[v][e] = ab[v][e] = 0.0f;
     }
     auto load = [&](RowIn<DT, V, KEPT> &r, uint32_t row) {
-        row = row < live_rows ? row : live_rows - 1;
+        row = team_row<LANES>(row < live_rows ? row : live_rows - 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = column(v);
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     int turn = 0;
     for (uint32_t base = group * TEAMS; base < live_rows; base += step) {  // the same for the workgroup
         const bool mine = base + team < live_rows;
-        const uint32_t row = mine ? base + team : live_rows - 1;
+        const uint32_t row = team_row<LANES>(mine ? base + team : live_rows - 1);
         if constexpr (AHEAD > 0) {
             r = next[0];
 #pragma unroll
@@ -345,8 +345,8 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
             oct_unpack<WT>(w[v], wf);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dy[e] = r.rstd * (dy[e] * wf[e] - __builtin_fmaf(t[e], m2, m1));
-            if constexpr (TINY) oct_store<DT>(dx + (size_t)row * d + c, dy, d - c);
-            else oct_store<DT>(dx + (size_t)row * d + (c < d - 8 ? c : d - 8), dy, 8);
+            if constexpr (TINY) oct_store<DT>(dx + (size_t)row * d + (uint32_t)c, dy, d - c);
+            else oct_store<DT>(dx + (size_t)row * d + (uint32_t)(c < d - 8 ? c : d - 8), dy, 8);
         }
     }
     if constexpr (STAGE == SUMS) return;
@@ -444,7 +444,6 @@ struct Forward {
     int32_t rows, d;
     float eps;
     const int32_t *live;
-    int cus;
     hipStream_t stream;
 };
 
@@ -456,7 +455,7 @@ hipError_t forward_as(const Forward &a) {
     const dim3 grid((uint32_t)(((int64_t)a.rows + TEAMS - 1) / TEAMS)), block(BLOCK);
     const auto kernel = a.codes != nullptr ? forward_kernel<DT, WIDE, T, true> : forward_kernel<DT, WIDE, T, false>;
     return launch_kernel(kernel, grid, block, a.stream, (const S *)a.in, (const WS *)a.weight, (const WS *)a.bias,
-                         (S *)a.out, (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, a.eps, a.live);
+                         (S *)a.out, (uint8_t *)a.codes, a.scales, a.stats, a.rows, a.d, a.eps, 1.0 / a.d, a.live);
 }
 
 template <int DT, bool WIDE>
@@ -516,6 +515,10 @@ hipError_t backward_dt(const Backward &a) {
 
 }  // namespace
 
+int layer_norm_lanes(int64_t d) {
+    return by_width(d, [](auto t) { return decltype(t)::LANES; });
+}
+
 int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus) {
     auto teams_of = [](auto t) { return (int64_t)(BACK_BLOCK / decltype(t)::LANES); };
     const int64_t teams = f32 ? by_width_backward<true>(d, teams_of) : by_width_backward<false>(d, teams_of);
@@ -530,8 +533,8 @@ size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups) {
 
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
                              void *codes, float *scales, float *stats, int32_t rows, int32_t d, float eps,
-                             const int32_t *live, int cus, hipStream_t stream) {
-    const Forward a{in, weight, bias, out, codes, scales, stats, rows, d, eps, live, cus, stream};
+                             const int32_t *live, hipStream_t stream) {
+    const Forward a{in, weight, bias, out, codes, scales, stats, rows, d, eps, live, stream};
     switch (dtype) {
     case DT_F32: return forward_dt<DT_F32, true>(a);
     case DT_F16: return wide ? forward_dt<DT_F16, true>(a) : forward_dt<DT_F16, false>(a);

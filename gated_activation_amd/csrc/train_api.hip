@@ -55,8 +55,8 @@ ga_status check_sizes(const char *op, int64_t rows, int64_t d, int64_t most_d, i
 
 int64_t blocks_of(int64_t d) { return (d + GA_CHECKPOINT_BLOCK - 1) / GA_CHECKPOINT_BLOCK; }
 
-// Elementwise kernels number the blocks of 128 values in 31 bits; the row
-// kernels' launches have at most 2^32 work-items (64 `waves` a row).
+// Elementwise kernels number the blocks of 128 values in 31 bits; the launches
+// of kernels that give a row `lanes` work-items have fewer than 2^32.
 ga_status check_blocks(const char *op, int64_t blocks) {
     if (blocks > INT32_MAX)
         return fail(GA_EUNSUPPORTED, "%s: %lld blocks of 128 values in one call (2^31 or more)", op, (long long)blocks);
@@ -123,13 +123,12 @@ ga_status layer_norm(const char *op, const void *in, const void *weight, const v
                               {"stats", stats, (size_t)rows * 8, 4, true, false},
                               {"codes", codes, keep ? n : 0, 1, true, !keep},
                               {"scales", scales, keep ? (size_t)rows * blocks_of(d) * 4 : 0, 4, true, !keep}};
-    if ((st = check_regions(op, regions)) != GA_OK) return st;
+    if ((st = check_regions(op, regions)) != GA_OK || (st = check_items(op, rows, ga::layer_norm_lanes(d))) != GA_OK)
+        return st;
     if (rows == 0) return GA_OK;
-    int cus = 0;
-    if ((st = usable_cus(&cus)) != GA_OK) return st;
     return ga::launched(op, ga::launch_layer_norm(dtype, weight_dtype == GA_F32, in, weight, bias, out,
                                                   keep ? codes : nullptr, scales, stats, (int32_t)rows, (int32_t)d, eps,
-                                                  live_rows, cus, (hipStream_t)stream));
+                                                  live_rows, (hipStream_t)stream));
 }
 
 ga_status layer_norm_backward(const char *op, const void *dout, const void *in, const void *codes, const float *scales,

@@ -373,7 +373,8 @@ typedef enum {
  * The activation's forward pass that keeps its input: one pass over in,
  * writing out [rows, d] (the value of the forward-only entry points, up to
  * fp32 rounding) and codes and scales of in (two halves; one for
- * SQUARED_RELU).  GELU_SPARSE: t = fp32(gate - cutoff) is kept in place of the
+ * SQUARED_RELU).  Limits as for ga_checkpoint_store; GELU_SPARSE as for
+ * ga_gelu_and_mul_sparse (fewer than 2^32 work-items, 64 to 1024 a row).  GELU_SPARSE: t = fp32(gate - cutoff) is kept in place of the
  * gate, with codes of at least 1 where t > 0, so the backward pass masks
  * exactly the values that the forward pass did; cutoff and std (statistics in
  * fp64) go to stats, which the others do not use (NULL).
@@ -405,6 +406,8 @@ ga_status ga_activation_backward_checkpoint(const void *dout, const void *codes,
  *     r = 1 / sqrt(v + eps), out = (in - m) r weight + bias
  * stats [rows, 2] = (m, r).  weight and bias (NULL: none) [d] are of
  * weight_dtype, which is dtype or GA_F32.  d <= GA_LAYER_NORM_MAX_D; eps >= 0.
+ * A launch has 16 to 1024 work-items a row (16 up to d = 128, 64 up to 1024);
+ * where they would reach 2^32 the call returns GA_EUNSUPPORTED.
  * _checkpoint also keeps fp32(in - m) in codes and scales (one half).
  */
 #define GA_LAYER_NORM_MAX_D 32768

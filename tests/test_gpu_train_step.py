@@ -198,6 +198,18 @@ def test_two_streams_at_once():
                 assert torch.equal(a, w), f"stream {i} output {k}"
 
 
+def test_tensors_on_a_device_that_is_not_current(monkeypatch):
+    """The binding makes the tensors' device current for the launch (here told that another one is)."""
+    from gated_activation_amd import _train
+    p, b = _everything_inputs(5), _buffers()
+    want = [t.clone() for t in _everything(p, b)]
+    monkeypatch.setattr(_train, "_current_device", lambda: -1)
+    got = _everything(p, _buffers())
+    torch.cuda.synchronize()
+    for a, w in zip(got, want):
+        assert torch.equal(a, w)
+
+
 def test_empty_arrays():
     z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
     for act in ga.ACTIVATIONS:
@@ -226,6 +238,10 @@ def test_refusals_on_the_device():
         ga.activation_backward(z(4, 8), ga.checkpoint_store(x), "silu")          # one half where two are needed
     with pytest.raises(ValueError):
         ga.activation_backward(z(4, 8), ga.Checkpoint(z(4, 2, 8, t=torch.int8), z(4, 2, 1)), "gelu_sparse")  # no stats
+    for act, kept in (("silu", ga.activation_checkpoint(z(4, 32), "gelu_sparse")[1]),
+                      ("squared_relu", ga.layer_norm_checkpoint(x, z(16))[1])):  # codes relative to their rows
+        with pytest.raises(ValueError):
+            ga.activation_backward(x, kept, act)
     with pytest.raises(ga.GaError):
         ga.activation_backward(x, x, "squared_relu", out=x)                      # in place
     with pytest.raises(ValueError):

@@ -114,7 +114,7 @@ def test_malformed(call, kwargs):
 @pytest.mark.parametrize("call,kwargs", [
     (norm, dict(d=32769)), (norm_back, dict(d=40000)), (balance, dict(e=1025)), (balance, dict(rows=2 ** 30, k=2)),
     (store, dict(rows=2 ** 30, d=300)), (backward, dict(rows=2 ** 30, d=300)), (forward, dict(rows=2 ** 22, d=16384, act=4)),
-    (backward, dict(rows=2 ** 26, d=1, act=4)),
+    (backward, dict(rows=2 ** 26, d=1, act=4)), (norm, dict(rows=2 ** 28, d=100)), (norm, dict(rows=2 ** 26, d=512)),
     (restore, dict(rows=2 ** 30, d=128, halves=2))])
 def test_unsupported(call, kwargs):
     assert call(**kwargs) == EUNSUP
