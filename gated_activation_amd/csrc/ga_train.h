@@ -416,9 +416,17 @@ __device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
     }
 }
 
-// Adds an octet's x - x0 and (x - x0)^2 to fp64 sums.  Differences of 16-bit
-// values are exact in fp32 up to 2^-24 of x0, and so are their sums of eight,
-// far below what decides a rounding of the row's result; squares go to fp64.
+// The value a row's sums are taken from: the median of its first, middle and
+// last, so that one value far out is not it.
+template <int DT>
+__device__ __forceinline__ float row_pivot(const typename Elem<DT>::storage *row, int d) {
+    return __builtin_amdgcn_fmed3f(Elem<DT>::to_f32(row[0]), Elem<DT>::to_f32(row[d / 2]), Elem<DT>::to_f32(row[d - 1]));
+}
+
+// Adds an octet's x - x0 and (x - x0)^2 to fp64 sums.  16-bit rows form the
+// difference and the sum of eight in fp32: exact but for values whose bits do
+// not overlap, and then within 2^-24 of the larger, which is of the row's
+// spread around x0; squares and the octets' sums are fp64.
 template <int DT>
 __device__ __forceinline__ void add_shifted(const float (&x)[8], float x0, double &s1, double &s2) {
     if constexpr (DT == DT_F32) {
@@ -454,7 +462,7 @@ template <int DT> struct RowOrigin {
 };
 
 // Mean and population variance of d values from the sums of x - x0 and of its
-// square, x0 being the row's first value: one pass, one reduction, and a row
+// square, x0 being the row's pivot: one pass, one reduction, and a row
 // of one repeated value has variance 0 exactly.  In fp64 the differences of
 // fp32 values are exact or carry 2^-53, and the subtraction loses at most
 // (mean - x0)^2 / var <= d <= 2^16 times that.

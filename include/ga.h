@@ -376,8 +376,7 @@ typedef enum {
  * SQUARED_RELU).  Limits as for ga_checkpoint_store; GELU_SPARSE as for
  * ga_gelu_and_mul_sparse (fewer than 2^32 work-items, 64 to 1024 a row).  GELU_SPARSE: t = fp32(gate - cutoff) is kept in place of the
  * gate, with codes of at least 1 where t > 0, so the backward pass masks
- * exactly the values that the forward pass did; cutoff and std (statistics in
- * fp64) go to stats, which the others do not use (NULL).
+ * exactly the values that the forward pass did; cutoff and std go to stats, which the others do not use (NULL).
  */
 ga_status ga_activation_checkpoint(const void *in, void *out, void *codes, float *scales, float *stats, int64_t rows,
                                    int64_t d, int32_t dtype, int32_t activation, float z, const int32_t *live_rows,
@@ -390,8 +389,10 @@ ga_status ga_activation_checkpoint(const void *in, void *out, void *codes, float
  * q = dout up gelu'(t) where t > 0 and 0 elsewhere, G the row's sum of q:
  *     dgate = q - (G / d) (1 + z (gate - m) / s), dup = dout gelu(max(t, 0))
  * the gradient through the row's mean and std too; the term with s is 0 where
- * s is 0, as the derivative of a std that is 0 is taken to be.  Statistics and
- * the side of the cutoff are fp64.
+ * s is 0, as the derivative of a std that is 0 is taken to be.  The row's
+ * statistics are summed in fp64 from differences to one of its values (16-bit
+ * rows form those, and gate - cutoff, in fp32), so the side of the cutoff that a
+ * value is on does not hang on an fp32 sum.
  * _checkpoint: the same formulas at the values that codes, scales (and stats)
  * stand for.
  */

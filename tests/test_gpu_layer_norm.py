@@ -143,3 +143,21 @@ def test_gradient_against_differences():
         assert abs((dw * v[0]).sum() - (((ga.layer_norm(xg, wg + h * vg[0], bg)[0].double()
                                           - ga.layer_norm(xg, wg - h * vg[0], bg)[0].double()).cpu().numpy() * de).sum()
                                         / (2 * h))) <= np.abs(de).sum() * 32 * ref.U / h
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_rows_with_one_value_far_out(dtype):
+    """A first value 3000 spreads out: the statistics of the rest do not suffer."""
+    d = 4096
+    rng = np.random.default_rng(11)
+    x = rng.normal(0, 1, (3, d)).astype(np.float32)
+    x[0, 0], x[1, d // 2], x[2, d - 1] = 3000.0, -3000.0, 3000.0
+    t = torch.from_numpy(x).to(TYPES[dtype])
+    y, st = ga.layer_norm(t.cuda(), torch.ones(d, device="cuda"))
+    torch.cuda.synchronize()
+    want, bound, mean, rstd = ref.layer_norm(t.double().numpy(), np.ones(d), np.zeros(d), EPS, dtype)
+    # differences to the pivot and their sums of eight: 2^-24 of 3000 in one octet of 512, of 8 elsewhere
+    moved = (3000.0 / 512 + 8.0) * 2.0 ** -24
+    close(st[:, :1], mean, 2 * ref.U * np.abs(mean) + moved, "mean")
+    close(st[:, 1:], rstd, 4 * ref.U * rstd, "rstd")
+    close(y, want, bound + rstd * moved, "y")
