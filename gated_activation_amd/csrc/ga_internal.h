@@ -166,14 +166,14 @@ hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *w
                              const int32_t *live, hipStream_t stream);
 // Groups of rows in the backward's launch, each of which leaves one partial row
 // of the weight's and the bias' gradient in the workspace ([groups, 2, d] fp32;
-// none with one group), after two sums for each strip of rows that are cut into
-// strips.  kept: from codes and scales, else from in.
+// none with one group), after two sums of each row for each 8192 columns where
+// a row is wider.  kept: from codes and scales, else from in.
 int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus);
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups);
 hipError_t launch_layer_norm_backward(int dtype, bool wide, const void *dout, const void *in, const void *codes,
                                       const float *scales, const float *stats, const void *weight, void *dx,
                                       void *dweight, void *dbias, bool kept, int32_t rows, int32_t d,
-                                      const int32_t *live, int groups, float *workspace, hipStream_t stream);
+                                      const int32_t *live, int groups, int cus, float *workspace, hipStream_t stream);
 
 // Balance loss, E <= BALANCE_MAX_E experts.  wide_index: int64 indices.
 constexpr int64_t BALANCE_MAX_E = 1024;

@@ -173,15 +173,21 @@ auto by_width_backward(int64_t d, F &&f) {
     return f(Team<512, 2>());
 }
 
-// Rows wider than a workgroup's 512 lanes of two octets are cut into strips of
-// STRIP columns and read twice: SUMS leaves each strip's part of a row's two
-// sums in the workspace, APPLY adds a row's parts and does the rest for its
-// strip's columns.  (Four and eight octets a lane, one pass, spilled: 2048 rows
-// of 16384, bf16 from codes, took 80 us, 1024 rows of 32768 414 us, against
-// 62 us either way.)
-constexpr int STRIP = 8192;
+// Rows wider than a workgroup's 512 lanes of two octets are cut into strips and
+// read twice.  SUMS leaves each 8192-column strip's part of a row's two sums in
+// the workspace; APPLY adds a row's parts and does the rest for strips of 1024
+// columns, a wavefront to a row, so that a workgroup adds up eight rows and few
+// partials are left.  (Four and eight octets a lane, one pass, spilled: 2048
+// rows of 16384, bf16 from codes, took 80 us, 1024 rows of 32768 414 us, against
+// 52 us either way; APPLY in strips of 8192 columns took 33 us for 311 rows of
+// 20897, from x, against 23 us.)
 enum Stage { WHOLE, SUMS, APPLY };
-constexpr int64_t strips_of(int64_t d) { return (d + STRIP - 1) / STRIP; }
+using SumsTeam = Team<512, 2>;
+using ApplyTeam = Team<64, 2>;
+template <typename T> constexpr int64_t strips_of(int64_t d) {
+    return (d + T::LANES * T::V * 8 - 1) / (T::LANES * T::V * 8);
+}
+inline bool in_strips(int64_t d) { return strips_of<SumsTeam>(d) > 1; }
 
 // Rows a team has in flight beside the one it works on, as the registers allow.
 template <int DT, int V> constexpr int rows_ahead() { return V * (DT == DT_F32 ? 2 : 1) <= 2 ? 1 : 0; }
@@ -221,12 +227,12 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
     // workgroups are numbered by group and strip
-    const uint32_t strips = STAGE == WHOLE ? 1 : (uint32_t)strips_of(d);
+    const uint32_t strips = STAGE == WHOLE ? 1 : (uint32_t)strips_of<T>(d);
     const uint32_t strip = STAGE == WHOLE ? 0 : blockIdx.x % strips;
     const uint32_t group = STAGE == WHOLE ? blockIdx.x : blockIdx.x / strips;
     const uint32_t groups = STAGE == WHOLE ? gridDim.x : gridDim.x / strips;
-    const int first = STAGE == WHOLE ? 0 : (int)strip * STRIP + (int)lane * 8;
-    auto column = [&](int v) { return STAGE == WHOLE ? (int)(v * LANES + lane) * 8 : first + v * LANES * 8; };
+    const int left = STAGE == WHOLE ? 0 : (int)strip * (LANES * V * 8);  // the strip's first column
+    auto column = [&](int v) { return left + (int)(v * LANES + lane) * 8; };
     const uint32_t step = groups * TEAMS;
     const uint32_t nb = ((uint32_t)d + BLOCK8 - 1) / BLOCK8;
     const float inv_d = 1.0f / (float)d;
@@ -330,8 +336,9 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
         }
         if constexpr (STAGE == APPLY) {
             s1 = s2 = 0.0f;
-            for (uint32_t i = 0; i < strips; ++i) {
-                const float2 p = row_sums[(size_t)row * strips + i];
+            const uint32_t parts_of_row = (uint32_t)strips_of<SumsTeam>(d);
+            for (uint32_t i = 0; i < parts_of_row; ++i) {
+                const float2 p = row_sums[(size_t)row * parts_of_row + i];
                 s1 += p.x;
                 s2 += p.y;
             }
@@ -410,7 +417,7 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
 #pragma unroll
                 for (int g = 0; g < WAVES / TEAM_WAVES; ++g)
                     t += parts[((g * TEAM_WAVES + cl / COLS) * 16 + which * 8 + e) * (COLS + 1) + cl % COLS];
-                const int c = (int)(v * LANES + cl) * 8, drop = TINY ? 0 : c - (d - 8);
+                const int c = left + (int)(v * LANES + cl) * 8, drop = TINY ? 0 : c - (d - 8);
                 const int col = (drop > 0 ? d - 8 : c) + (int)e;
                 if ((int)e >= drop && col < d) put((int)which, col, t);
             }
@@ -478,7 +485,7 @@ struct Backward {
     bool kept;
     int32_t rows, d;
     const int32_t *live;
-    int groups;
+    int groups, cus;
     float *workspace;
     hipStream_t stream;
 };
@@ -488,25 +495,28 @@ hipError_t backward_as(const Backward &a) {
     using S = typename Elem<DT>::storage;
     constexpr int WT = weight_type<DT, WIDE>();
     using WS = typename Elem<WT>::storage;
-    const int64_t strips = strips_of(a.d);
+    const bool wide = in_strips(a.d);
     float2 *row_sums = (float2 *)a.workspace;
-    float *partial = a.workspace + (strips > 1 ? 2 * strips * a.rows : 0);
-    const dim3 grid((uint32_t)(a.groups * strips)), block(BACK_BLOCK);
-    auto launch = [&](auto kept, auto stage) {
-        constexpr bool KEPT = decltype(kept)::value;
-        return launch_kernel(backward_kernel<DT, WIDE, T, KEPT, decltype(stage)::value>, grid, block, a.stream,
-                             (const S *)a.dout, (const S *)a.in, (const uint8_t *)a.codes, a.scales, a.stats,
-                             (const WS *)a.weight, (S *)a.dx, (WS *)a.dweight, (WS *)a.dbias, partial, row_sums, a.rows,
-                             a.d, a.live);
+    float *partial = a.workspace + (wide ? 2 * strips_of<SumsTeam>(a.d) * a.rows : 0);
+    auto launch = [&](auto kept, auto team, auto stage, int64_t grid) {
+        return launch_kernel(backward_kernel<DT, WIDE, decltype(team), decltype(kept)::value, decltype(stage)::value>,
+                             dim3((uint32_t)grid), dim3(BACK_BLOCK), a.stream, (const S *)a.dout, (const S *)a.in,
+                             (const uint8_t *)a.codes, a.scales, a.stats, (const WS *)a.weight, (S *)a.dx,
+                             (WS *)a.dweight, (WS *)a.dbias, partial, row_sums, a.rows, a.d, a.live);
     };
     auto launches = [&](auto kept) {
-        if constexpr (T::LANES * T::V * 8 == STRIP) {
-            if (strips > 1) {
-                const hipError_t e = launch(kept, std::integral_constant<Stage, SUMS>());
-                return e != hipSuccess ? e : launch(kept, std::integral_constant<Stage, APPLY>());
+        if constexpr (std::is_same<T, SumsTeam>::value) {
+            if (wide) {
+                // two workgroups to a compute unit: no sums over rows here
+                const int64_t strips = strips_of<T>(a.d), most = 2 * a.cus / strips, rows = a.rows < 1 ? 1 : a.rows;
+                const hipError_t e = launch(kept, T(), std::integral_constant<Stage, SUMS>(),
+                                            strips * (rows < most ? rows : most));
+                if (e != hipSuccess) return e;
+                return launch(kept, ApplyTeam(), std::integral_constant<Stage, APPLY>(),
+                              strips_of<ApplyTeam>(a.d) * a.groups);
             }
         }
-        return launch(kept, std::integral_constant<Stage, WHOLE>());
+        return launch(kept, T(), std::integral_constant<Stage, WHOLE>(), a.groups);
     };
     const hipError_t e = a.kept ? launches(std::true_type()) : launches(std::false_type());
     if (e != hipSuccess || a.groups == 1) return e;
@@ -529,13 +539,15 @@ int layer_norm_lanes(int64_t d) {
 int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus) {
     auto teams_of = [](auto t) { return (int64_t)(BACK_BLOCK / decltype(t)::LANES); };
     const int64_t teams = f32 ? by_width_backward<true>(d, teams_of) : by_width_backward<false>(d, teams_of);
-    const int64_t need = (rows + teams - 1) / teams, most = cus > strips_of(d) ? cus / strips_of(d) : 1;
+    const int64_t strips = in_strips(d) ? strips_of<ApplyTeam>(d) : 1;
+    const int64_t of = in_strips(d) ? BACK_BLOCK / ApplyTeam::LANES : teams;
+    const int64_t need = (rows + of - 1) / of, most = cus > strips ? cus / strips : 1;
     return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups) {
-    const int64_t strips = strips_of(d);
-    return (groups > 1 ? (size_t)groups * 2 * (size_t)d * 4 : 0) + (strips > 1 ? (size_t)rows * (size_t)strips * 8 : 0);
+    return (groups > 1 ? (size_t)groups * 2 * (size_t)d * 4 : 0) +
+           (in_strips(d) ? (size_t)rows * (size_t)strips_of<SumsTeam>(d) * 8 : 0);
 }
 
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,
@@ -553,8 +565,8 @@ hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *w
 hipError_t launch_layer_norm_backward(int dtype, bool wide, const void *dout, const void *in, const void *codes,
                                       const float *scales, const float *stats, const void *weight, void *dx,
                                       void *dweight, void *dbias, bool kept, int32_t rows, int32_t d,
-                                      const int32_t *live, int groups, float *workspace, hipStream_t stream) {
-    const Backward a{dout, in, codes, scales, stats, weight, dx, dweight, dbias, kept, rows, d, live, groups,
+                                      const int32_t *live, int groups, int cus, float *workspace, hipStream_t stream) {
+    const Backward a{dout, in, codes, scales, stats, weight, dx, dweight, dbias, kept, rows, d, live, groups, cus,
                      workspace, stream};
     switch (dtype) {
     case DT_F32: return backward_dt<DT_F32, true>(a);

@@ -159,7 +159,7 @@ ga_status layer_norm_backward(const char *op, const void *dout, const void *in, 
     return ga::launched(op, ga::launch_layer_norm_backward(
                                 dtype, weight_dtype == GA_F32, dout, kept ? nullptr : in, kept ? codes : nullptr, scales,
                                 stats, weight, dx, dweight, dbias, kept, (int32_t)rows, (int32_t)d, live_rows,
-                                ga::layer_norm_groups(rows, d, dtype == GA_F32, cus), (float *)workspace, (hipStream_t)stream));
+                                ga::layer_norm_groups(rows, d, dtype == GA_F32, cus), cus, (float *)workspace, (hipStream_t)stream));
 }
 
 ga_status check_balance(const char *op, int64_t rows, int64_t experts, int64_t k, int32_t dtype, float coefficient) {
