@@ -248,8 +248,9 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     float unused = 0.0f;
     team_sum2<64 * W>(total, unused, sums);
     const float share = total * (float)inv_d;
-    const float b = s == 0.0f ? 0.0f : share * z / s;
-    const float a = s == 0.0f ? share : __builtin_fmaf(share, z * z, share);
+    // (no gradient, no share of it: z * z may be past fp32's range)
+    const float b = s == 0.0f || share == 0.0f ? 0.0f : share * z / s;
+    const float a = s == 0.0f || share == 0.0f ? share : __builtin_fmaf(share, z * z, share);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * 64 * W + at.lane) * 8;

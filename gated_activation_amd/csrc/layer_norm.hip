@@ -206,7 +206,6 @@ template <int DT, int V, bool KEPT> struct RowIn {
 // on the row's last eight values instead: those of them that other lanes own
 // are left out of the sums, and stored with the very bits their owners store.
 // A team past the last row does that row again, out of the columns' sums.
-
 template <int DT, bool WIDE, typename T, bool KEPT, Stage STAGE>
 __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     const typename Elem<DT>::storage *__restrict__ dout, const typename Elem<DT>::storage *__restrict__ in,

@@ -61,6 +61,25 @@ def test_many_tokens_and_the_same_bits():
     assert torch.equal(a.loss, b.loss) and torch.equal(a.counts, b.counts)
 
 
+def test_gradient_against_differences():
+    """The kernel's own loss, differenced along random directions in fp32."""
+    rng = np.random.default_rng(5)
+    logits, le = values(rng, (40, 12), "fp32")
+    index = torch.from_numpy(rng.integers(0, 12, (40, 2))).cuda()
+    h = 2.0 ** -5
+    b = ga.balance_loss(logits.cuda(), index)
+    g = ga.balance_loss_backward(logits.cuda(), b).double().cpu().numpy()
+    for _ in range(4):
+        v = rng.normal(0, 1, le.shape).astype(np.float32)
+        vg = torch.from_numpy(v).cuda()
+        plus, minus = (float(ga.balance_loss(logits.cuda() + s * h * vg, index).loss) for s in (1, -1))
+        # a softmax' third derivative along v is at most 8 max|v|^3 of a mean of counts (the loss, about 1), over
+        # 6; the loss carries (n + 100) roundings
+        slack = 1.5 * (h * h * 8 * np.abs(v).max() ** 3 / 6 + 140 * ref.U / h)
+        assert abs((g * v).sum() - (plus - minus) / (2 * h)) <= slack
+        assert np.abs(g * v).sum() > 4 * 140 * ref.U / h
+
+
 def test_even_router_has_the_coefficient_as_its_loss():
     experts, k = 16, 2
     index = torch.arange(64 * k, device="cuda").reshape(64, k) % experts

@@ -225,6 +225,46 @@ def test_sparse_rows_without_spread_or_finite_values():
     assert float(out.abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("z", [-3.0, 0.0, 8.0, 1e25])
+def test_sparse_multipliers(z):
+    """Every value past the cutoff, half of them, none (and a multiplier whose square fp32 cannot hold)."""
+    rng = np.random.default_rng(17)
+    x, xe = values(rng, (4, 2 * 900), "fp32")
+    dout, de = values(rng, (4, 900), "fp32")
+    z32 = float(np.float32(z))
+    out, c = ga.activation_checkpoint(x.cuda(), "gelu_sparse", z=z)
+    wx, dx = (ga.activation_backward(dout.cuda(), k, "gelu_sparse", z=z) for k in (x.cuda(), c))
+    torch.cuda.synchronize()
+    want, bound = ref.forward("gelu_sparse", xe, "fp32", z32)
+    close(out, want, bound, "out")
+    t, _, std = ref.over_cutoff(xe[:, :900], z32)
+    assert z != -3.0 or (t > 0).mean() > 0.99
+    want, bound = ref.sparse_backward(de, t, std, xe[:, 900:], z32, "fp32")
+    close(wx, want, bound, "dx from x")
+    if z >= 8.0:
+        assert float(out.abs().max()) == 0.0 and float(wx.abs().max()) == 0.0 and float(dx.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("act", ELEMENTWISE)
+def test_gradient_against_differences(act):
+    """The kernel's own forward pass, differenced along random directions in fp32."""
+    rows, d, h, halves = 5, 96, 2.0 ** -6, ref.halves(act)
+    rng = np.random.default_rng(21)
+    x, xe = values(rng, (rows, halves * d), "fp32")
+    dout, de = values(rng, (rows, d), "fp32")
+    dx = ga.activation_backward(dout.cuda(), x.cuda(), act).double().cpu().numpy()
+    for _ in range(4):
+        v = np.sign(rng.normal(0, 1, x.shape)).astype(np.float32)
+        plus, minus = (ga.activation_checkpoint(x.cuda() + s * h * torch.from_numpy(v).cuda(), act)[0].double() for s in (1, -1))
+        moved = ((plus - minus).cpu().numpy() * de).sum() / (2 * h)
+        # along +-1: third derivatives of f(gate) up below 2 + 3 |up| (h^2 / 6 of them; squared ReLU: a second
+        # derivative that jumps by 2 where it passes zero within h), forward errors of 32 u of (1 + |x|)^2 over h
+        size = (1 + np.abs(xe[:, :d])) * (1 + np.abs(xe[:, -d:]))
+        slack = (np.abs(de) * (h * h * (2 + 3 * np.abs(xe[:, -d:])) + 32 * ref.U * size / h)).sum()
+        slack += (np.abs(de) * h * 2 * (np.abs(xe) < h)).sum() if act == "squared_relu" else 0.0
+        assert abs((dx * v).sum() - moved) <= slack
+
+
 def test_many_rows_past_one_launch_of_blocks():
     """More blocks of 128 than rows: the numbering of a wide array of many rows, spot rows exactly."""
     rows, d = 70000, 257
