@@ -42,7 +42,9 @@ template <int DT, bool WIDE> constexpr int weight_type() { return WIDE ? DT_F32 
 
 // The team of a row by its width: LANES lanes of V octets.  Two octets a lane
 // halve what the row's reductions cost a value; a row of up to 1024 values is
-// a wavefront's own and needs no barrier.
+// a wavefront's own and needs no barrier.  Four octets a lane for the forward
+// took 34.7 us for 38.2 at 4096 x 8192 bf16 with codes, but 35.4 for 34.3 at
+// 4096 columns, 33.6 for 32.9 at 2048, and 3.0 for 2.4 for a single row.
 template <int LANES_, int V_, bool TINY_ = false> struct Team {
     static constexpr int LANES = LANES_, V = V_;
     static constexpr bool TINY = TINY_;  // rows of fewer than eight values
