@@ -245,7 +245,7 @@ __global__ __launch_bounds__(FLAT_BLOCK) void backward_kernel(
                 oct_store<DT>(dx + at + d, v, n[k]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = 2.0f * __builtin_fmaxf(x[e], 0.0f) * t[e];
+                for (int e = 0; e < 8; ++e) a[e] = 2.0f * above_zero<KEPT>(x[e]) * t[e];
                 oct_store<DT>(dx + at, a, n[k]);
             }
         }

@@ -338,6 +338,14 @@ __device__ __forceinline__ void block_decode(uint2 c, float scale, float (&f)[8]
         f[e] = __builtin_fmaf((float)((w[e >> 2] >> ((e & 3) * 8)) & 0xFFu), scale, base);
 }
 
+// max(x, 0).  A NaN gives 0, as in the forward pass; restored from codes (KEPT)
+// it stays NaN, since a block's NaN scale stands for finite values too.
+template <bool KEPT>
+__device__ __forceinline__ float above_zero(float x) {
+    if constexpr (KEPT) return __builtin_elementwise_maximum(x, 0.0f);
+    else return __builtin_fmaxf(x, 0.0f);
+}
+
 // ---------------------------------------------------------------------------
 // Row sums in fp64 (as fast as fp32 on this device outside packed math): lanes
 // paired as in wave_sum, so the result is the same on every lane.

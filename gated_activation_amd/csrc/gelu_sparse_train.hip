@@ -232,7 +232,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float f, df;
-            gelu_tanh_slope(__builtin_fmaxf(t[e], 0.0f), f, df);
+            gelu_tanh_slope(above_zero<KEPT>(t[e]), f, df);
             q[v][e] = t[e] > 0.0f ? dv[e] * up[e] * df : 0.0f;
             asm volatile("" : "+v"(q[v][e]));  // else its factors are kept for a later fma: twice the registers
             du[e] = dv[e] * f;

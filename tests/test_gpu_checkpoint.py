@@ -93,6 +93,35 @@ def test_unusual_blocks(dtype):
     assert (got[0] == 0).all() and (got[3, :128] == 0).all()
 
 
+@pytest.mark.parametrize("d", [5, 400])
+@pytest.mark.parametrize("bad", [np.inf, np.nan, 2.0 ** 126])
+@pytest.mark.parametrize("act", ELEMENTWISE)
+def test_backward_of_a_bad_block_is_nan(act, bad, d):
+    """The gradients from a gate block whose scale is NaN are NaN, other blocks' are not."""
+    h = ref.halves(act)
+    x = torch.full((3, h * d), -1.0)
+    x[1, min(d - 1, 130)] = float(bad)
+    first, last = (0, d) if d <= 128 else (128, 256)
+    dout = torch.ones(3, d)
+    for dtype in (torch.bfloat16, torch.float32):
+        _, c = ga.activation_checkpoint(x.to(dtype).cuda(), act)
+        dx = ga.activation_backward(dout.to(dtype).cuda(), c, act).float().cpu().numpy()
+        nan = np.isnan(dx).reshape(3, h, d)
+        assert nan[1, :, first:last].all() and nan.sum() == h * (last - first), (act, bad, dtype)
+
+
+@pytest.mark.parametrize("d", [300, 3000])
+def test_sparse_backward_of_a_bad_block_is_nan(d):
+    """A gate block whose scale is NaN: both halves' gradients of it, though nothing of it is above the cutoff."""
+    x = torch.randn(3, 2 * d, generator=torch.Generator().manual_seed(5))
+    dout = torch.ones(3, d)
+    _, c = ga.activation_checkpoint(x.cuda(), "gelu_sparse", z=Z)
+    c.scales[1, 0, 1] = float("nan")
+    dx = ga.activation_backward(dout.cuda(), c, "gelu_sparse", z=Z).cpu().numpy().reshape(3, 2, d)
+    nan = np.isnan(dx)
+    assert nan[1, :, 128:256].all() and not nan[[0, 2]].any() and not nan[1, 1, 256:].any()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("act", ELEMENTWISE)
 @pytest.mark.parametrize("rows,d,offset,live", SHAPES)
