@@ -233,7 +233,9 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         for (int e = 0; e < 8; ++e) {
             float f, df;
             gelu_tanh_slope(above_zero<KEPT>(t[e]), f, df);
-            q[v][e] = t[e] > 0.0f ? dv[e] * up[e] * df : 0.0f;
+            // a restored NaN stands for a value whose side is lost: it goes into the row's sum
+            const bool on = KEPT ? !(t[e] <= 0.0f) : t[e] > 0.0f;
+            q[v][e] = on ? dv[e] * up[e] * df : 0.0f;
             asm volatile("" : "+v"(q[v][e]));  // else its factors are kept for a later fma: twice the registers
             du[e] = dv[e] * f;
             total += q[v][e];
