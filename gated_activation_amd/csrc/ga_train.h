@@ -431,28 +431,17 @@ __device__ __forceinline__ float row_pivot(const typename Elem<DT>::storage *row
     return __builtin_amdgcn_fmed3f(Elem<DT>::to_f32(row[0]), Elem<DT>::to_f32(row[d / 2]), Elem<DT>::to_f32(row[d - 1]));
 }
 
-// Adds an octet's x - x0 and (x - x0)^2 to fp64 sums.  16-bit rows form the
-// difference and the sum of eight in fp32: exact but for values whose bits do
-// not overlap, and then within 2^-24 of the larger, which is of the row's
-// spread around x0; squares and the octets' sums are fp64.
-template <int DT>
+// Adds an octet's x - x0 and (x - x0)^2 to fp64 sums.  The differences are
+// fp64 for 16-bit rows too: the pivot may be far out (two of the three values it
+// is the median of), and fp32 differences to it would then carry 2^-24 of it,
+// one-sided where many values are alike: 1.4e-3 of the mean for rows of 1.46e-3
+// with 60000 in those places.
 __device__ __forceinline__ void add_shifted(const float (&x)[8], float x0, double &s1, double &s2) {
-    if constexpr (DT == DT_F32) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double a = (double)x[e] - (double)x0;
-            s1 += a;
-            s2 = __builtin_fma(a, a, s2);
-        }
-    } else {
-        float a[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            a[e] = x[e] - x0;
-            const double b = a[e];
-            s2 = __builtin_fma(b, b, s2);
-        }
-        s1 += (double)(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
+    for (int e = 0; e < 8; ++e) {
+        const double a = (double)x[e] - (double)x0;
+        s1 += a;
+        s2 = __builtin_fma(a, a, s2);
     }
 }
 

@@ -63,7 +63,7 @@ __device__ __forceinline__ void gate_moments(const Oct<DT> (&g)[V], uint32_t lan
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] : first;
         }
-        add_shifted<DT>(x, first, s1, s2);
+        add_shifted(x, first, s1, s2);
     }
     team_sum2<64 * W>(s1, s2, slots);
     shifted_moments(s1, s2, (double)first, inv_d, mean, var);
@@ -126,7 +126,11 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     float *row_scales = scales + (size_t)at.row * 2 * nb;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = (int)(v * 64 * W + at.lane) * 8;
+        uint32_t lane = at.lane;
+        // columns formed again: kept from the gate's loads, eight of them spill, and a load of up then waits for
+        // its address behind the stores of the octet before
+        if constexpr (!EARLY) asm volatile("" : "+v"(lane));
+        const int c = (int)(v * 64 * W + lane) * 8;
         const int n = d - c;
         const uint32_t block = (uint32_t)c / BLOCK8;
         if constexpr (!EARLY) {

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : first;
         }
-        add_shifted<DT>(f, first, s1, s2);
+        add_shifted(f, first, s1, s2);
     }
     team_sum2<LANES>(s1, s2, slots[team]);
     if (!mine) return;

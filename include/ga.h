@@ -390,9 +390,10 @@ ga_status ga_activation_checkpoint(const void *in, void *out, void *codes, float
  *     dgate = q - (G / d) (1 + z (gate - m) / s), dup = dout gelu(max(t, 0))
  * the gradient through the row's mean and std too; the term with s is 0 where
  * s is 0, as the derivative of a std that is 0 is taken to be.  The row's
- * statistics are summed in fp64 from differences to one of its values (16-bit
- * rows form those, and gate - cutoff, in fp32), so the side of the cutoff that a
- * value is on does not hang on an fp32 sum.
+ * statistics are summed in fp64 from fp64 differences to one of its values, and
+ * gate - cutoff is formed in fp32 from the cutoff as two fp32 numbers (16-bit
+ * rows; in fp64 else), which keeps its sign: the side of the cutoff that a value
+ * is on does not hang on an fp32 sum.
  * _checkpoint: the same formulas at the values that codes, scales (and stats)
  * stand for.  What is formed from a block whose scale is NaN is NaN (max(NaN, 0)
  * of a NaN in `in` itself is 0).  GELU_SPARSE: a gate block's NaN scale makes the

@@ -47,3 +47,39 @@ def test_an_up_block_past_the_codes_counts_where_the_gate_passes():
     dx = ga.activation_backward(torch.ones(2, d, device="cuda"), c, "gelu_sparse", z=Z).cpu().numpy().reshape(2, 2, d)
     assert np.isfinite(dx[0]).all() and (dx[0, 0] != 0).any()
     assert np.isnan(dx[1, 0]).all() and np.isfinite(dx[1, 1]).all()
+
+
+# ---- the cutoff's side -------------------------------------------------------------
+
+@pytest.mark.parametrize("above", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [400, 4096, 16384])
+def test_the_cutoffs_side_where_the_sampled_values_are_far_out(d, dtype, above):
+    """First, middle and last value 60000, the others 0.00146, four values of 100 and a multiplier that puts the
+    cutoff 7e-4 past them or short of them: differences to 60000 in fp32 would move the mean by 1.4e-3."""
+    x = torch.full((1, 2 * d), 1.0)
+    x[0, :d] = 0.00146
+    at = [9, 77, d // 2 + 30, d - 20]
+    x[0, at] = 100.0
+    x[0, [0, d // 2, d - 1]] = 60000.0
+    x = x.to(TYPES[dtype])
+    g = x[0, :d].double().numpy()
+    mean = math.fsum(g) / d
+    std = math.sqrt(math.fsum((g - mean) ** 2) / d)
+    z = float(np.float32((g[9] + (-7e-4 if above else 7e-4) - mean) / std))
+    # an fp32 multiplier puts the cutoff within 2^-24 |z| s <= 2.1e-5 of that
+    assert 6.7e-4 < abs(g[9] - (mean + z * std)) < 7.3e-4 and (g[9] > mean + z * std) == above
+    xg, dg = x.cuda(), torch.ones(1, d, dtype=TYPES[dtype], device="cuda")
+    out, c = ga.activation_checkpoint(xg, "gelu_sparse", z=z)
+    dx = ga.activation_backward(dg, c, "gelu_sparse", z=z)
+    wx = ga.activation_backward(dg, xg, "gelu_sparse", z=z)
+    torch.cuda.synchronize()
+    on = np.zeros(d, bool)
+    on[[0, d // 2, d - 1] + (at if above else [])] = True
+    assert np.array_equal((c.codes[0, 0] > 0).cpu().numpy(), on)
+    assert np.array_equal((out[0] > 0).cpu().numpy(), on)
+    for v in (dx, wx):   # dup = gelu(max(t, 0))
+        assert np.array_equal((v[0, d:] > 0).cpu().numpy(), on)
+    y, st = ga.layer_norm(xg[:, :d].contiguous(), torch.ones(d, device="cuda"))
+    torch.cuda.synchronize()
+    assert abs(float(st[0, 0]) - mean) <= 2 * ref.U * mean
