@@ -166,7 +166,7 @@ hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *w
                              const int32_t *live, hipStream_t stream);
 // Groups of rows in the backward's launch, each of which leaves one partial row
 // of the weight's and the bias' gradient in the workspace ([groups, 2, d] fp32;
-// none with one group), after two sums of each row for each 8192 columns where
+// none with one group), after three sums of each row for each 8192 columns where
 // a row is wider.  kept: from codes and scales, else from in.
 int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus);
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups);

@@ -393,35 +393,40 @@ __device__ __forceinline__ uint32_t team_row(uint32_t row) {
     else return row;
 }
 
-// Sums of two values over the team that shares a row: 16 lanes, a wavefront,
-// or LANES / 64 wavefronts of a workgroup (all of whose teams call it together).
-// `slots`: LDS of the team's own, 2 * LANES / 64 values that nothing else
+// Sums of N values over the team that shares a row: 16 lanes, a wavefront, or
+// LANES / 64 wavefronts of a workgroup (all of whose teams call it together).
+// `slots`: LDS of the team's own, N * LANES / 64 values that nothing else
 // touches until the next barrier after this call.
+template <int LANES, int N, typename T>
+__device__ __forceinline__ void team_sums(T (&v)[N], T *slots) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if constexpr (LANES == 16) v[k] = row16_sum(v[k]);
+        else v[k] = wave_sum(v[k]);
+    }
+    if constexpr (LANES > 64) {
+        constexpr int W = LANES / 64;
+        const int wave = (threadIdx.x % LANES) >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) slots[N * wave + k] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = slots[k];
+#pragma unroll
+        for (int i = 1; i < W; ++i)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += slots[N * i + k];
+    }
+}
+
 template <int LANES, typename T>
 __device__ __forceinline__ void team_sum2(T &a, T &b, T *slots) {
-    if constexpr (LANES == 16) {
-        a = row16_sum(a);
-        b = row16_sum(b);
-    } else {
-        a = wave_sum(a);
-        b = wave_sum(b);
-        if constexpr (LANES > 64) {
-            constexpr int W = LANES / 64;
-            const int wave = (threadIdx.x % LANES) >> 6;
-            if ((threadIdx.x & 63) == 0) {
-                slots[2 * wave] = a;
-                slots[2 * wave + 1] = b;
-            }
-            __syncthreads();
-            a = slots[0];
-            b = slots[1];
-#pragma unroll
-            for (int i = 1; i < W; ++i) {
-                a += slots[2 * i];
-                b += slots[2 * i + 1];
-            }
-        }
-    }
+    T v[2] = {a, b};
+    team_sums<LANES>(v, slots);
+    a = v[0];
+    b = v[1];
 }
 
 // The value a row's sums are taken from: the median of its first, middle and

@@ -9,6 +9,11 @@
 //     dw_i = sum over rows of dy_i n_i, db_i = sum over rows of dy_i
 // with n from x and (m, r), or r times the value its code stands for.
 //
+// m comes as an fp32 number.  Where the mean is far above the spread its
+// rounding would be in every n of a row (3.75e-3 at mean 65536.3 and spread 1),
+// so the backward from x also sums x - m over the row and takes the mean of that
+// off again (off_centre).
+//
 // Both are bound by HBM.  A team of lanes (a 16-lane DPP row, a wavefront, or
 // a workgroup) holds a row in registers, V octets a lane, so a row is read
 // once.  The statistics are fp64 (shifted_moments): one reduction, exact for a
@@ -176,7 +181,7 @@ auto by_width_backward(int64_t d, F &&f) {
 }
 
 // Rows wider than a workgroup's 512 lanes of two octets are cut into strips and
-// read twice.  SUMS leaves each 8192-column strip's part of a row's two sums in
+// read twice.  SUMS leaves each 8192-column strip's part of a row's sums in
 // the workspace; APPLY adds a row's parts and does the rest for strips of 1024
 // columns, a wavefront to a row, so that a workgroup adds up eight rows and few
 // partials are left.  (Four and eight octets a lane, one pass, spilled: 2048
@@ -189,10 +194,21 @@ using ApplyTeam = Team<64, 2>;
 template <typename T> constexpr int64_t strips_of(int64_t d) {
     return (d + T::LANES * T::V * 8 - 1) / (T::LANES * T::V * 8);
 }
+constexpr int ROW_SUMS = 3;  // floats of a row and strip, at most
 inline bool in_strips(int64_t d) { return strips_of<SumsTeam>(d) > 1; }
 
 // Rows a team has in flight beside the one it works on, as the registers allow.
 template <int DT, int V> constexpr int rows_ahead() { return V * (DT == DT_F32 ? 2 : 1) <= 2 ? 1 : 0; }
+
+// The row's mean less the fp32 m it came as, from the sum of x - m.  Taken where
+// |m| r > 4, with n off by 2^-22 otherwise, which is of the order of the other
+// roundings of n; a sum of more than m's rounding can leave (and a few roundings
+// of a mean that was itself summed in fp32) means that m is not meant to be the
+// row's mean, and m is used as it is.
+__device__ __forceinline__ float off_centre(float sum, float inv_d, float m, float r) {
+    const float off = sum * inv_d, size = __builtin_fabsf(m);
+    return size * r > 4.0f && __builtin_fabsf(off) <= 0x1p-22f * size ? off : 0.0f;
+}
 
 // What a team reads of a row.
 template <int DT, int V, bool KEPT> struct RowIn {
@@ -215,7 +231,7 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     const typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ weight, typename Elem<DT>::storage *__restrict__ dx,
     typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dweight,
     typename Elem<weight_type<DT, WIDE>()>::storage *__restrict__ dbias, float *__restrict__ partial,
-    float2 *__restrict__ row_sums, int32_t rows, int32_t d, const int32_t *__restrict__ live) {
+    float *__restrict__ row_sums, int32_t rows, int32_t d, const int32_t *__restrict__ live) {
     constexpr int WT = weight_type<DT, WIDE>();
     constexpr int LANES = T::LANES, V = T::V;
     constexpr bool TINY = T::TINY;
@@ -223,7 +239,8 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
     constexpr int TEAM_WAVES = LANES > 64 ? LANES / 64 : 1;
     constexpr int COLS = LANES > 64 ? 64 : LANES;  // lanes of a wave that own different columns
     constexpr int AHEAD = rows_ahead<DT, V>();
-    __shared__ float slots[2][TEAMS][2 * TEAM_WAVES];
+    constexpr int SUMMED = KEPT ? 2 : 3;
+    __shared__ float slots[2][TEAMS][SUMMED * TEAM_WAVES];
     __shared__ float parts[TEAMS > 1 ? WAVES * 16 * (COLS + 1) : 1];
     const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const uint32_t live_rows = live != nullptr ? (uint32_t)clamp_live(live, rows) : (uint32_t)rows;
@@ -305,7 +322,7 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
         } else {
             load(r, row);
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        float s[SUMMED] = {};  // of dy w, of dy w n and, from x, of x - m
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int drop = dropped(v);  // elements that are other lanes'
@@ -323,8 +340,9 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float n = t[e] * r.rstd, dv = dy[e] * wf[e];
-                s1 += dv;
-                s2 = __builtin_fmaf(dv, n, s2);
+                s[0] += dv;
+                s[1] = __builtin_fmaf(dv, n, s[1]);
+                if constexpr (!KEPT) s[2] += TINY && column(v) + e >= d ? 0.0f : t[e];
                 a[e] = n;
             }
             if (STAGE != SUMS && mine) {
@@ -336,28 +354,46 @@ __global__ __launch_bounds__(BACK_BLOCK, 2) void backward_kernel(
             }
         }
         if constexpr (STAGE == APPLY) {
-            s1 = s2 = 0.0f;
             const uint32_t parts_of_row = (uint32_t)strips_of<SumsTeam>(d);
-            for (uint32_t i = 0; i < parts_of_row; ++i) {
-                const float2 p = row_sums[(size_t)row * parts_of_row + i];
-                s1 += p.x;
-                s2 += p.y;
+            const float *part = row_sums + (size_t)row * parts_of_row * SUMMED;
+#pragma unroll
+            for (int k = 0; k < SUMMED; ++k) s[k] = 0.0f;
+            for (uint32_t i = 0; i < parts_of_row; ++i, part += SUMMED) {
+#pragma unroll
+                for (int k = 0; k < SUMMED; ++k) s[k] += part[k];
             }
         } else {
-            team_sum2<LANES>(s1, s2, slots[turn][team]);
+            team_sums<LANES>(s, slots[turn][team]);
             turn ^= 1;
         }
         if constexpr (STAGE == SUMS) {
-            if (lane == 0) row_sums[(size_t)row * strips + strip] = float2{s1, s2};
+            if (lane == 0) {
+                float *part = row_sums + ((size_t)row * strips + strip) * SUMMED;
+#pragma unroll
+                for (int k = 0; k < SUMMED; ++k) part[k] = s[k];
+            }
             continue;
         }
-        const float m1 = s1 * inv_d, m2 = s2 * inv_d * r.rstd;
+        float off = 0.0f;
+        if constexpr (!KEPT) {
+            off = off_centre(s[2], inv_d, r.mean, r.rstd);
+            if (off != 0.0f) s[1] = __builtin_fmaf(-off * r.rstd, s[0], s[1]);
+        }
+        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d * r.rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = column(v);
             float dy[8], t[8], wf[8];
             octet(r, v, dy, t);
             oct_unpack<WT>(w[v], wf);
+            if (!KEPT && off != 0.0f) {
+                const int drop = mine ? dropped(v) : 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    t[e] -= off;
+                    aw[v][e] = __builtin_fmaf(e < drop ? 0.0f : dy[e], -off * r.rstd, aw[v][e]);
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) dy[e] = r.rstd * (dy[e] * wf[e] - __builtin_fmaf(t[e], m2, m1));
             if constexpr (TINY) oct_store<DT>(dx + (size_t)row * d + (uint32_t)c, dy, d - c);
@@ -497,8 +533,8 @@ hipError_t backward_as(const Backward &a) {
     constexpr int WT = weight_type<DT, WIDE>();
     using WS = typename Elem<WT>::storage;
     const bool wide = in_strips(a.d);
-    float2 *row_sums = (float2 *)a.workspace;
-    float *partial = a.workspace + (wide ? 2 * strips_of<SumsTeam>(a.d) * a.rows : 0);
+    float *row_sums = a.workspace;
+    float *partial = a.workspace + (wide ? ROW_SUMS * strips_of<SumsTeam>(a.d) * a.rows : 0);
     auto launch = [&](auto kept, auto team, auto stage, int64_t grid) {
         return launch_kernel(backward_kernel<DT, WIDE, decltype(team), decltype(kept)::value, decltype(stage)::value>,
                              dim3((uint32_t)grid), dim3(BACK_BLOCK), a.stream, (const S *)a.dout, (const S *)a.in,
@@ -548,7 +584,7 @@ int layer_norm_groups(int64_t rows, int64_t d, bool f32, int cus) {
 
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t d, int groups) {
     return (groups > 1 ? (size_t)groups * 2 * (size_t)d * 4 : 0) +
-           (in_strips(d) ? (size_t)rows * (size_t)strips_of<SumsTeam>(d) * 8 : 0);
+           (in_strips(d) ? (size_t)rows * (size_t)strips_of<SumsTeam>(d) * ROW_SUMS * 4 : 0);
 }
 
 hipError_t launch_layer_norm(int dtype, bool wide, const void *in, const void *weight, const void *bias, void *out,

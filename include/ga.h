@@ -429,7 +429,9 @@ ga_status ga_layer_norm_checkpoint(const void *in, const void *weight, const voi
  *     dx = r (v - mean(v) - n mean(v n)) per row
  *     dweight = sum over live rows of dout n, dbias = sum of dout (NULL: not wanted)
  * dx of dtype, dweight and dbias of weight_dtype, sums in fp32.  No live rows:
- * dweight and dbias are zero.
+ * dweight and dbias are zero.  m is the mean that stats hold in fp32; where
+ * |m| r > 4, so that its rounding would show, the mean of in - m is taken off n
+ * again if it is no more than that rounding (2^-22 |m|).
  *   workspace  ga_layer_norm_backward_workspace_bytes(rows, d) bytes, 16-byte
  *              aligned, any content; calls that share one must not overlap in
  *              time.

@@ -83,3 +83,45 @@ def test_the_cutoffs_side_where_the_sampled_values_are_far_out(d, dtype, above):
     y, st = ga.layer_norm(xg[:, :d].contiguous(), torch.ones(d, device="cuda"))
     torch.cuda.synchronize()
     assert abs(float(st[0, 0]) - mean) <= 2 * ref.U * mean
+
+
+# ---- layer norm: a mean far above the spread ------------------------------------------
+
+def _offset_rows(rng, rows, d, dtype, mean, spread):
+    if spread is not None:
+        return values(rng, (rows, d), dtype, mean=mean, std=spread)
+    x = torch.ones(rows, d, dtype=TYPES[dtype])            # one step of the type in one place of each row
+    x[torch.arange(rows), torch.from_numpy(rng.integers(0, d, rows))] += 2 * ref.HALF_EPS[dtype]
+    return x, x.double().numpy()
+
+
+@pytest.mark.parametrize("dtype,mean,spread", [("fp32", 65536.3, 1.0), ("fp32", -4096.1, 0.5), ("fp32", 300.7, 1.0),
+                                               ("fp16", 1.0, None), ("bf16", 1.0, None)])
+@pytest.mark.parametrize("rows,d", [(64, 5), (70, 100), (40, 500), (64, 1000), (33, 2000), (20, 4000), (12, 8192),
+                                    (9, 20000)])
+def test_backward_from_x_where_the_mean_is_far_above_the_spread(rows, d, dtype, mean, spread):
+    """n is taken from the row's own mean, not from its rounding to fp32 in stats, which would add the same amount
+    (up to 2^-25 of the mean, in spreads) to every n of a row: 3.75e-3 at mean 65536.3 and spread 1."""
+    rng = np.random.default_rng(rows + d)
+    x, xe = _offset_rows(rng, rows, d, dtype, mean, spread)
+    dy, de = values(rng, (rows, d), dtype, mean=0.5)
+    if dtype == "fp16":                                    # r is up to 3e4: dx fits the type
+        dy = dy * 2.0 ** -4
+        de = dy.double().numpy()
+    w, we = values(rng, (d,), "fp32", mean=1.0, std=0.3)
+    xg, wg = x.cuda(), w.cuda()
+    _, st = ga.layer_norm(xg, wg, eps=1e-12)
+    dx, dw, db = ga.layer_norm_backward(dy.cuda(), xg, wg, stats=st)
+    torch.cuda.synchronize()
+    r = st[:, 1:].double().cpu().numpy()
+    t = xe - xe.mean(1, keepdims=True)
+    assert (np.abs(xe.mean(1, keepdims=True) * r) > 16).all()
+    (wx, ww, wb), bounds = ref.layer_norm_backward(de, t * r, r, we, dtype, "fp32", 32)
+    # x - mean is exact or rounded by u of itself; the mean of those differences to the fp32 mean is the sum of d
+    # terms of at most |t| + the mean's rounding (2 u of it), added 32 one after another and then by pairs
+    off = 72 * ref.U * (np.abs(t) + 2 * ref.U * np.abs(xe)).mean(1, keepdims=True) * r + 2 * ref.U * np.abs(t) * r
+    v = np.abs(de * we)
+    extra = r * (off * (v * np.abs(t * r)).mean(1, keepdims=True) + np.abs(t * r) * (v * off).mean(1, keepdims=True))
+    close(dx, wx, bounds[0] + extra, "dx")
+    close(dw, ww, bounds[1] + (np.abs(de) * off).sum(0), "dw")
+    close(db, wb, bounds[2], "db")
