@@ -8,8 +8,12 @@
 //     dgate_i = q_i - (G / d) (1 + z (gate_i - m) / s)
 //     dup_i   = dout_i gelu_tanh(max(t_i, 0))
 // (the second term of the bracket is the derivative of s; a row without spread
-// has s = 0 and the term is taken as 0).  gate - m is t + z s, so
-// dgate_i = q_i - A - B t_i with two numbers A, B a row.
+// has s = 0 and the term is taken as 0).  From x that is q_i - A - B (gate_i - m)
+// with A = G / d and B = A z / s, two numbers a row.  From codes gate - m is
+// t + z s, and with A = (1 + z^2) G / d it is q_i - A - B t_i; from x that form
+// would lose z^2 roundings of t for nothing.  B (gate - m) is formed with both
+// scaled by the power of two of 1 / s: z / s alone passes fp32's range where a
+// row has next to no spread.
 //
 // gelu_tanh'(0) is 1/2, so the gradient jumps where the gate passes the
 // cutoff: the side is decided from sums in fp64, which runs at fp32's rate here
@@ -75,12 +79,12 @@ __device__ __forceinline__ void trim_all(Oct<DT> (&o)[V], uint32_t lane, int d) 
     for (int v = 0; v < V; ++v) oct_trim<DT, TINY>(o[v], (int)(v * 64 * W + lane) * 8, d);
 }
 
-// fp32(gate - cutoff) of an octet; 0 past the row's end.
+// fp32(gate - at) of an octet, at the cutoff or the mean; 0 past the row's end.
 template <int DT>
-__device__ __forceinline__ void over_cutoff(const Oct<DT> &g, const RowOrigin<DT> &cutoff, int n, float (&t)[8]) {
+__device__ __forceinline__ void less(const Oct<DT> &g, const RowOrigin<DT> &at, int n, float (&t)[8]) {
     oct_unpack<DT>(g, t);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = cutoff.from(t[e]);
+    for (int e = 0; e < 8; ++e) t[e] = at.from(t[e]);
     if (n < 8) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = e < n ? t[e] : 0.0f;
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         }
         if (block >= nb) continue;  // the same for the 16 lanes of a block
         float t[8], up[8], scale;
-        over_cutoff<DT>(g[v], cutoff, n, t);
+        less<DT>(g[v], cutoff, n, t);
         const uint2 ct = block_encode<difference_of<DT>(), true>(t, scale);
         codes_store(row_codes + (uint32_t)c, ct, n);
         if ((at.lane & 15) == 0) row_scales[block] = scale;
@@ -187,14 +191,14 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
             oct_fetch<DT, TINY>(u[v], in + row2 + d, c, d);
         }
     };
-    RowOrigin<DT> cutoff(0.0);
-    float s;
+    RowOrigin<DT> cutoff(0.0), middle(0.0);
+    double std;
     if constexpr (KEPT) {
         if constexpr (EARLY) {
 #pragma unroll
             for (int v = 0; v < V; ++v) load(v);
         }
-        s = stats[2 * (size_t)at.row + 1];
+        std = stats[2 * (size_t)at.row + 1];
     } else {
         const typename Elem<DT>::storage *x = in + row2;
 #pragma unroll
@@ -209,9 +213,9 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         gate_moments<DT, W, V>(g, at.lane, d, inv_d, first, slots, mean, var);
 #pragma unroll
         for (int v = 0; v < V; ++v) stay_raw(g[v]);
-        const double std = __builtin_sqrt(var);
+        std = __builtin_sqrt(var);
         cutoff = RowOrigin<DT>(__builtin_fma((double)z, std, mean));
-        s = (float)std;
+        middle = RowOrigin<DT>(mean);
     }
     float q[V][8], total = 0.0f;
 #pragma unroll
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
             block_decode(cu[v], su[v], up);
         } else {
             oct_trim<DT, TINY>(u[v], c, d);
-            over_cutoff<DT>(g[v], cutoff, n, t);
+            less<DT>(g[v], cutoff, n, t);
             oct_unpack<DT>(u[v], up);
         }
         oct_unpack<DT>(o[v], dv);
@@ -254,9 +258,14 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
     float unused = 0.0f;
     team_sum2<64 * W>(total, unused, sums);
     const float share = total * (float)inv_d;
+    // unit = 2^-e for std in [2^e, 2^(e+1)), e within fp32's normal exponents
+    int e2 = (int)(__builtin_bit_cast(uint64_t, std) >> 52) - 1023;
+    e2 = e2 < -126 ? -126 : e2 > 126 ? 126 : e2;
+    const float unit = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
     // (no gradient, no share of it: z * z may be past fp32's range)
-    const float b = s == 0.0f || share == 0.0f ? 0.0f : share * z / s;
-    const float a = s == 0.0f || share == 0.0f ? share : __builtin_fmaf(share, z * z, share);
+    const bool alone = std == 0.0 || share == 0.0f;
+    const float b = alone ? 0.0f : share * z * (float)(1.0 / (std * (double)unit));
+    const float a = !KEPT || alone ? share : __builtin_fmaf(share, z * z, share);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (int)(v * 64 * W + at.lane) * 8;
@@ -265,9 +274,9 @@ __global__ __launch_bounds__(team_block<W>(), (sparse_waves<DT, W, V>())) void s
         if (n <= 0) continue;
         float t[8];
         if constexpr (KEPT) block_decode(ct[v], st[v], t);
-        else over_cutoff<DT>(g[v], cutoff, n, t);
+        else less<DT>(g[v], middle, n, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = q[v][e] - __builtin_fmaf(b, t[e], a);
+        for (int e = 0; e < 8; ++e) t[e] = q[v][e] - __builtin_fmaf(b, t[e] * unit, a);
         oct_store<DT>(dx + row2 + (uint32_t)c, t, n);
     }
 }

@@ -125,3 +125,100 @@ def test_backward_from_x_where_the_mean_is_far_above_the_spread(rows, d, dtype, 
     close(dx, wx, bounds[0] + extra, "dx")
     close(dw, ww, bounds[1] + (np.abs(de) * off).sum(0), "dw")
     close(db, wb, bounds[2], "db")
+
+
+# ---- sparse GELU: multipliers and spreads far out -----------------------------------------
+
+def _sparse_from_x(gate, up, dout, z, dtype):
+    """dx from x with the statistics' term from gate - mean, and bounds that do not grow with z^2."""
+    d = gate.shape[1]
+    t, _, std = ref.over_cutoff(gate, z)
+    f, df, bf, bdf = ref.activation("gelu_tanh", np.maximum(t, 0.0))
+    on = t > 0
+    # past 10 the sigmoid is 1 to 2^-120: f = t, f' = 1 but for the roundings of the products
+    bf, bdf = np.where(t > 10, 4 * ref.U * np.abs(f), bf), np.where(t > 10, 4 * ref.U, bdf)
+    moved = np.where(t > 10, 0.0, 2 * ref.U * np.abs(t))  # what t's own rounding does to f'
+    q = np.where(on, dout * up * df, 0.0)
+    bq = np.where(on, np.abs(dout * up) * (bdf + 3 * ref.U * np.abs(df) + moved), 0.0)
+    total = q.sum(1, keepdims=True)
+    btotal = bq.sum(1, keepdims=True) + 90 * ref.U * np.abs(q).sum(1, keepdims=True)
+    n = (gate - gate.mean(1, keepdims=True)) / std
+    size = 1.0 + np.abs(z * n)
+    dg = q - total / d * (1.0 + z * n)
+    bg = bq + (btotal / d + np.abs(total) / d * 8 * ref.U) * size + 2 * ref.U * np.abs(q)
+    du = dout * f
+    bu = np.abs(dout) * (bf + 2 * ref.U * np.abs(f) + 2 * ref.U * np.abs(df * t) * on)
+    return (np.concatenate([dg, du], 1),
+            np.concatenate([bg + ref.rounding(dg, dtype), bu + ref.rounding(du, dtype)], 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("z", [-1e4, -60.0, -3.0, 0.0])
+@pytest.mark.parametrize("d", [5, 900, 6000, 16400])
+def test_sparse_from_x_with_every_value_past_the_cutoff(d, z, dtype):
+    """The term of the row's std is z times a normalised gate: its error grows with z, not with z^2 as where it is
+    formed from gate - cutoff."""
+    rng = np.random.default_rng(d)
+    x, xe = values(rng, (3, 2 * d), dtype)
+    dout, de = values(rng, (3, d), dtype, mean=0.5)
+    z32 = float(np.float32(z))
+    if dtype == "fp16" and z < -100.0:
+        dout = dout * 2.0 ** -6                           # dup is dout times 1e4
+        de = dout.double().numpy()
+    wx = ga.activation_backward(dout.cuda(), x.cuda(), "gelu_sparse", z=z)
+    torch.cuda.synchronize()
+    want, bound = _sparse_from_x(xe[:, :d], xe[:, d:], de, z32, dtype)
+    close(wx, want, bound, "dx from x")
+
+
+@pytest.mark.parametrize("dtype,spread", [("fp32", 1e-37), ("fp32", 2.0 ** -133), ("bf16", 1e-37)])
+def test_sparse_from_x_with_next_to_no_spread(dtype, spread):
+    """z / std alone is past fp32's range times the row's sum; z n is not."""
+    d = 700
+    rng = np.random.default_rng(3)
+    x, _ = values(rng, (3, 2 * d), "fp32")
+    x[:, :d] *= spread
+    x = x.to(TYPES[dtype])
+    xe = x.double().numpy()
+    dout, de = values(rng, (3, d), dtype, mean=900.0, std=9000.0)
+    wx = ga.activation_backward(dout.cuda(), x.cuda(), "gelu_sparse", z=Z)
+    torch.cuda.synchronize()
+    want, bound = _sparse_from_x(xe[:, :d], xe[:, d:], de, Z, dtype)
+    assert np.abs(want).max() < 1e7 and np.abs(want[:, :d]).max() > 1.0
+    # gate - mean and gate - cutoff of subnormal numbers are rounded to a whole 2^-149
+    low = 2.0 ** -148
+    extra = np.abs(want).max() * 4 * Z * low / np.abs(xe[:, :d]).mean() + np.abs(np.tile(de, (1, 2))) * low
+    close(wx, want, bound + extra, "dx from x")
+
+
+@pytest.mark.parametrize("z", [-3.0, -1.0, 0.0, 0.5, 2.5])
+@pytest.mark.parametrize("d", [900, 6000])
+def test_sparse_from_codes_at_other_multipliers(d, z):
+    """As at the usual multiplier: the formulas at the values that the codes stand for."""
+    rng = np.random.default_rng(18)
+    x, xe = values(rng, (4, 2 * d), "fp32")
+    dout, de = values(rng, (4, d), "fp32", mean=0.3)
+    z32 = float(np.float32(z))
+    _, c = ga.activation_checkpoint(x.cuda(), "gelu_sparse", z=z)
+    dx = ga.activation_backward(dout.cuda(), c, "gelu_sparse", z=z)
+    torch.cuda.synchronize()
+    v = ref.decode(c.codes.cpu().numpy(), c.scales.cpu().numpy())
+    s32 = c.stats[:, 1:].double().cpu().numpy()
+    want, bound = ref.sparse_backward(de, v[:, 0], s32, v[:, 1], z32, "fp32")
+    # a restored value is rounded once in fp32: its slope may move by that much
+    extra = 4 * ref.U * np.tile(np.abs(de), (1, 2)) * (1 + np.abs(v[:, 0]).max()) * (2 + np.abs(v[:, 1]).max())
+    close(dx, want, bound + extra, "dx from codes")
+    q = np.where(v[:, 0] > 0, de * v[:, 1] * ref.activation("gelu_tanh", np.maximum(v[:, 0], 0.0))[1], 0.0)
+    assert (np.abs(q.sum(1)) / d * (1 + z * z) > 100 * bound[:, :d].mean(1)).any()   # the statistics' term shows
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [6, 700])
+def test_sparse_from_x_with_a_cutoff_past_fp32(d, dtype):
+    """Nothing is above it: no output and no gradient."""
+    x = torch.randn(2, 2 * d, generator=torch.Generator().manual_seed(4)) * 50
+    xg, z = x.to(TYPES[dtype]).cuda(), 3e38
+    out, _ = ga.activation_checkpoint(xg, "gelu_sparse", z=z)
+    wx = ga.activation_backward(torch.ones(2, d, dtype=TYPES[dtype], device="cuda"), xg, "gelu_sparse", z=z)
+    torch.cuda.synchronize()
+    assert float(out.abs().max()) == 0.0 and float(wx.abs().max()) == 0.0
