@@ -334,13 +334,21 @@ __global__ __launch_bounds__(BAL_BLOCK) void gradient_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(p[v][e], w[v][e], dot);
         dot = lanes_sum<L>(dot);
+        // the mean of the distances to it, once more: where one p is next to 1 the gradient is a small
+        // difference of counts, of which the first mean carries roundings of the counts themselves
+        float rest = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) rest = __builtin_fmaf(p[v][e], w[v][e] - dot, rest);
+        rest = lanes_sum<L>(rest);
         if (!in) continue;
         const bool use = mask == nullptr || mask[t] != 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (int)(v * L + lane) * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[v][e] = use ? factor * p[v][e] * (w[v][e] - dot) : 0.0f;
+            for (int e = 0; e < 8; ++e) p[v][e] = use ? factor * p[v][e] * ((w[v][e] - dot) - rest) : 0.0f;
             if (c < E) oct_store<DT>(dlogits + (size_t)t * E + c, p[v], E - c);
         }
     }

@@ -468,6 +468,8 @@ ga_status ga_layer_norm_backward_checkpoint(const void *dout, const void *codes,
  * Backward, with counts as constants and dloss a device fp32:
  *     dlogits = dloss coefficient experts / (k n^2) p (counts - sum_j counts[j] p[j])
  * rows of tokens that do not count get 0 (past the live count: untouched).
+ * (counts less their mean under p, formed again from the distances to it: a token
+ * with a probability next to 1 has small gradients, right to their own roundings)
  *   workspace  as for layer norm, ga_balance_loss_workspace_bytes() bytes.
  */
 #define GA_BALANCE_MAX_EXPERTS 1024

@@ -222,3 +222,32 @@ def test_sparse_from_x_with_a_cutoff_past_fp32(d, dtype):
     wx = ga.activation_backward(torch.ones(2, d, dtype=TYPES[dtype], device="cuda"), xg, "gelu_sparse", z=z)
     torch.cuda.synchronize()
     assert float(out.abs().max()) == 0.0 and float(wx.abs().max()) == 0.0
+
+
+# ---- balance loss: a probability next to one -------------------------------------------
+
+@pytest.mark.parametrize("experts", [3, 8, 40, 128, 300, 1000])
+def test_balance_gradient_where_one_probability_is_next_to_one(experts):
+    """The gradient of a token whose router is (almost) sure is p (counts - their mean under p): small numbers, off
+    by roundings of themselves and not of the counts."""
+    rows, k = 96, 2
+    rng = np.random.default_rng(experts)
+    logits = rng.normal(0, 1, (rows, experts)).astype(np.float32)
+    top = rng.integers(0, experts, rows)
+    logits[np.arange(rows), top] = 6.0 + np.linspace(0, 20, rows, dtype=np.float32) + np.float32(math.log(experts))
+    index = np.stack([top, np.minimum(rng.integers(0, experts, rows), experts // 3)], 1)
+    b = ga.balance_loss(torch.from_numpy(logits).cuda(), torch.from_numpy(index).cuda())
+    g = ga.balance_loss_backward(torch.from_numpy(logits).cuda(), b).double().cpu().numpy()
+    le = logits.astype(np.float64)
+    counts = np.bincount(index.reshape(-1), minlength=experts)
+    p = ref.softmax(le)
+    factor = experts / (k * rows * rows)
+    # counts less their mean under p, without cancellation: sum_j p_j (counts_e - counts_j)
+    apart = (counts[:, None] - counts[None, :]).astype(np.float64)
+    off, size = p @ apart.T, p @ np.abs(apart)
+    rel = ref.relative_softmax(le)
+    # p's own errors, those of the p_j in the mean and of a sum of up to 1024 terms, relative to the counts'
+    # distances from their mean; a first mean that is off by as much of the largest count counts twice so small
+    most = 2 * rel + 64 * ref.U
+    bound = factor * (p * (size * most + (counts.max() + 1) * most ** 2)) + 2.0 ** -149
+    close(torch.from_numpy(g), factor * p * off, bound, "dlogits")
