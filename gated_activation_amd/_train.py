@@ -47,10 +47,15 @@ _bind()
 class Checkpoint(NamedTuple):
     """An array kept in 8 bits: codes int8 [rows, d] or, gate and up apart,
     [rows, 2, d]; scales fp32 [rows, ceil(d / 128)] or [rows, 2, ceil(d / 128)];
-    stats fp32 [rows, 2] where the codes are relative to their row."""
+    stats fp32 [rows, 2] where the codes are relative to their row.  The one
+    that activation_checkpoint returns says whose input it is: the activation
+    and, of gelu_sparse, its z.  None (a Checkpoint made of tensors alone): the
+    caller's knowledge."""
     codes: torch.Tensor
     scales: torch.Tensor
     stats: Optional[torch.Tensor] = None
+    activation: Optional[str] = None
+    z: Optional[float] = None
 
 
 class Balance(NamedTuple):
@@ -117,14 +122,14 @@ def _live(live_rows, device, name):
     return live_rows.data_ptr()
 
 
-def _checkpoint(c, rows, halves, d, stats, device, name):
-    """The checkpoint's tensors, checked, or new ones where c is None."""
-    codes, scales, st = (None, None, None) if c is None else c
+def _checkpoint(c, rows, halves, d, stats, device, name, activation=None, z=None):
+    """A Checkpoint of c's tensors, checked, or of new ones where c is None."""
+    codes, scales, st = (None, None, None) if c is None else c[:3]
     lead = (rows,) if halves == 1 else (rows, halves)
     codes = _like(codes, lead + (d,), torch.int8, device, "checkpoint.codes", name)
     scales = _like(scales, lead + (-(-d // GA_CHECKPOINT_BLOCK),), torch.float32, device, "checkpoint.scales", name)
     st = _like(st, (rows, 2), torch.float32, device, "checkpoint.stats", name) if stats else None
-    return Checkpoint(codes, scales, st)
+    return Checkpoint(codes, scales, st, activation, z)
 
 
 def _given(c, stats, name):
@@ -179,7 +184,8 @@ def activation_checkpoint(x, activation, z=Z_SPARSITY_095, live_rows=None, out=N
     returns (out [rows, d], Checkpoint).  activation: "silu", "gelu_tanh",
     "gelu" (erf) or "gelu_sparse" (cutoff multiplier z) on x = [gate | up]
     ([rows, 2d]), or "squared_relu" on x [rows, d].  out and checkpoint: tensors
-    to write into; rows past live_rows stay as they are."""
+    to write into; rows past live_rows stay as they are.  The Checkpoint returned
+    knows its activation and z."""
     name = "activation_checkpoint"
     act = _activation(activation, name)
     _matrix(x, "x", name)
@@ -190,17 +196,19 @@ def activation_checkpoint(x, activation, z=Z_SPARSITY_095, live_rows=None, out=N
     d, device = cols // halves, x.device
     sparse = act == GA_ACT_GELU_SPARSE
     out = _like(out, (rows, d), x.dtype, device, "out", name)
-    c = _checkpoint(checkpoint, rows, halves, d, sparse, device, name)
+    c = _checkpoint(checkpoint, rows, halves, d, sparse, device, name, activation, float(z) if sparse else None)
     live = _live(live_rows, device, name)
     _call(lib.ga_activation_checkpoint, device, x.data_ptr(), out.data_ptr(), c.codes.data_ptr(), c.scales.data_ptr(),
           _ptr(c.stats), rows, d, _TORCH_DTYPE[x.dtype], act, z, live)
     return out, c
 
 
-def activation_backward(dout, kept, activation, z=Z_SPARSITY_095, live_rows=None, out=None):
+def activation_backward(dout, kept, activation, z=None, live_rows=None, out=None):
     """The gradient of a gated activation's input from dout [rows, d] and what
     the forward pass kept: the input x itself (of dout's dtype) or the
-    Checkpoint of activation_checkpoint.  Returns dx ([rows, 2d]; [rows, d] for
+    Checkpoint of activation_checkpoint.  z, of gelu_sparse: None is the
+    Checkpoint's own or, where it has none and with x, activation_checkpoint's
+    default.  A Checkpoint of another activation or z is refused.  Returns dx ([rows, 2d]; [rows, d] for
     "squared_relu"); rows past live_rows stay as they are."""
     name = "activation_backward"
     act = _activation(activation, name)
@@ -216,9 +224,18 @@ def activation_backward(dout, kept, activation, z=Z_SPARSITY_095, live_rows=None
         _given(kept, sparse, name)
         if not sparse and kept.stats is not None:
             raise ValueError(f"{name}: the Checkpoint's codes are relative to their rows (it has stats): not of {activation}")
+        if kept.activation is not None and kept.activation != activation:
+            raise ValueError(f"{name}: the Checkpoint is of {kept.activation}, not of {activation}")
+        if sparse and kept.z is not None:
+            # the kernels take z in fp32
+            if z is not None and z != kept.z and ctypes.c_float(z).value != ctypes.c_float(kept.z).value:
+                raise ValueError(f"{name}: the Checkpoint is of z = {kept.z}, not of {z}")
+            z = kept.z
         kept = _checkpoint(kept, rows, halves, d, sparse, device, name)
     out = _like(out, (rows, halves * d), dtype, device, "out", name)
     live = _live(live_rows, device, name)
+    if z is None:
+        z = Z_SPARSITY_095
     if from_x:
         _call(lib.ga_activation_backward, device, dout.data_ptr(), kept.data_ptr(), out.data_ptr(), rows, d,
               _TORCH_DTYPE[dtype], act, z, live)

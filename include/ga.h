@@ -395,10 +395,11 @@ ga_status ga_activation_checkpoint(const void *in, void *out, void *codes, float
  * rows; in fp64 else), which keeps its sign: the side of the cutoff that a value
  * is on does not hang on an fp32 sum.
  * _checkpoint: the same formulas at the values that codes, scales (and stats)
- * stand for.  What is formed from a block whose scale is NaN is NaN (max(NaN, 0)
- * of a NaN in `in` itself is 0).  GELU_SPARSE: a gate block's NaN scale makes the
- * row's G NaN, and with it every dgate of the row; an up block's does where one
- * of its values has t > 0, and nothing is formed from the others.
+ * stand for; activation and z are those of the forward pass.  What is formed from
+ * a block whose scale is NaN is NaN (max(NaN, 0) of a NaN in `in` itself is 0).
+ * GELU_SPARSE: a gate block's NaN scale makes the row's G NaN, and with it every
+ * dgate of the row; an up block's does where one of its values has t > 0, and
+ * nothing is formed from the others.
  */
 ga_status ga_activation_backward(const void *dout, const void *in, void *dx, int64_t rows, int64_t d, int32_t dtype,
                                  int32_t activation, float z, const int32_t *live_rows, ga_stream stream);

@@ -251,3 +251,41 @@ def test_balance_gradient_where_one_probability_is_next_to_one(experts):
     most = 2 * rel + 64 * ref.U
     bound = factor * (p * (size * most + (counts.max() + 1) * most ** 2)) + 2.0 ** -149
     close(torch.from_numpy(g), factor * p * off, bound, "dlogits")
+
+
+# ---- what a Checkpoint is of ---------------------------------------------------------------
+
+def test_a_checkpoint_knows_its_activation_and_multiplier():
+    """The backward pass takes the forward's z from it, and refuses another z or activation."""
+    x = torch.randn(6, 2 * 300, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    dout = torch.ones(6, 300, device="cuda")
+    _, c = ga.activation_checkpoint(x, "gelu_sparse", z=0.5)
+    assert c.activation == "gelu_sparse" and c.z == 0.5
+    want = ga.activation_backward(dout, ga.Checkpoint(*c[:3]), "gelu_sparse", z=0.5)   # of tensors alone
+    for z in (None, 0.5, np.float32(0.5)):
+        assert torch.equal(ga.activation_backward(dout, c, "gelu_sparse", z=z), want)
+    assert torch.equal(ga.activation_backward(dout, c, "gelu_sparse"), want)
+    with pytest.raises(ValueError):
+        ga.activation_backward(dout, c, "gelu_sparse", z=ga.Z_SPARSITY_095)
+    _, s = ga.activation_checkpoint(x, "silu")
+    assert s.activation == "silu" and s.z is None
+    for act in ("gelu", "gelu_tanh"):
+        with pytest.raises(ValueError):
+            ga.activation_backward(dout, s, act)
+    assert torch.equal(ga.activation_backward(dout, s, "silu", z=0.1), ga.activation_backward(dout, s, "silu"))
+    # written into another's tensors it is its own
+    _, again = ga.activation_checkpoint(x, "gelu", checkpoint=s)
+    assert again.activation == "gelu" and again.codes is s.codes
+    ga.activation_backward(dout, again, "gelu")
+    # from x and from tensors alone the default z is activation_checkpoint's
+    _, c = ga.activation_checkpoint(x, "gelu_sparse")
+    assert torch.equal(ga.activation_backward(dout, ga.Checkpoint(*c[:3]), "gelu_sparse"),
+                       ga.activation_backward(dout, c, "gelu_sparse"))
+    assert torch.equal(ga.activation_backward(dout, x, "gelu_sparse"),
+                       ga.activation_backward(dout, x, "gelu_sparse", z=ga.Z_SPARSITY_095))
+    # codes stored by themselves are of no activation
+    r = torch.randn(4, 40, device="cuda")
+    kept = ga.checkpoint_store(r)
+    assert kept.activation is None
+    ga.activation_backward(torch.ones_like(r), kept, "squared_relu")
+    torch.cuda.synchronize()
