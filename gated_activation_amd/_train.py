@@ -44,18 +44,26 @@ def _bind():
 _bind()
 
 
-class Checkpoint(NamedTuple):
-    """An array kept in 8 bits: codes int8 [rows, d] or, gate and up apart,
-    [rows, 2, d]; scales fp32 [rows, ceil(d / 128)] or [rows, 2, ceil(d / 128)];
-    stats fp32 [rows, 2] where the codes are relative to their row.  The one
-    that activation_checkpoint returns says whose input it is: the activation
-    and, of gelu_sparse, its z.  None (a Checkpoint made of tensors alone): the
-    caller's knowledge."""
+class _Arrays(NamedTuple):
     codes: torch.Tensor
     scales: torch.Tensor
     stats: Optional[torch.Tensor] = None
+
+
+class Checkpoint(_Arrays):
+    """An array kept in 8 bits, a tuple of three: codes int8 [rows, d] or, gate
+    and up apart, [rows, 2, d]; scales fp32 [rows, ceil(d / 128)] or [rows, 2,
+    ceil(d / 128)]; stats fp32 [rows, 2] where the codes are relative to their
+    row.  The one that activation_checkpoint returns says whose input it is, by
+    its attributes activation and, of gelu_sparse, z.  None (a Checkpoint made of
+    tensors alone): the caller's knowledge."""
     activation: Optional[str] = None
     z: Optional[float] = None
+
+    def _replace(self, **arrays):
+        c = super()._replace(**arrays)
+        c.activation, c.z = self.activation, self.z
+        return c
 
 
 class Balance(NamedTuple):
@@ -124,12 +132,15 @@ def _live(live_rows, device, name):
 
 def _checkpoint(c, rows, halves, d, stats, device, name, activation=None, z=None):
     """A Checkpoint of c's tensors, checked, or of new ones where c is None."""
-    codes, scales, st = (None, None, None) if c is None else c[:3]
+    codes, scales, st = (None, None, None) if c is None else c
     lead = (rows,) if halves == 1 else (rows, halves)
     codes = _like(codes, lead + (d,), torch.int8, device, "checkpoint.codes", name)
     scales = _like(scales, lead + (-(-d // GA_CHECKPOINT_BLOCK),), torch.float32, device, "checkpoint.scales", name)
     st = _like(st, (rows, 2), torch.float32, device, "checkpoint.stats", name) if stats else None
-    return Checkpoint(codes, scales, st, activation, z)
+    c = Checkpoint(codes, scales, st)
+    if activation is not None:
+        c.activation, c.z = activation, z
+    return c
 
 
 def _given(c, stats, name):

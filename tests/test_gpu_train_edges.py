@@ -261,7 +261,10 @@ def test_a_checkpoint_knows_its_activation_and_multiplier():
     dout = torch.ones(6, 300, device="cuda")
     _, c = ga.activation_checkpoint(x, "gelu_sparse", z=0.5)
     assert c.activation == "gelu_sparse" and c.z == 0.5
-    want = ga.activation_backward(dout, ga.Checkpoint(*c[:3]), "gelu_sparse", z=0.5)   # of tensors alone
+    codes, scales, stats = c                                                           # a tuple of three
+    want = ga.activation_backward(dout, ga.Checkpoint(codes, scales, stats), "gelu_sparse", z=0.5)  # of tensors alone
+    moved = c._replace(codes=codes.cpu().cuda())
+    assert moved.z == 0.5 and torch.equal(ga.activation_backward(dout, moved, "gelu_sparse"), want)
     for z in (None, 0.5, np.float32(0.5)):
         assert torch.equal(ga.activation_backward(dout, c, "gelu_sparse", z=z), want)
     assert torch.equal(ga.activation_backward(dout, c, "gelu_sparse"), want)
@@ -279,7 +282,7 @@ def test_a_checkpoint_knows_its_activation_and_multiplier():
     ga.activation_backward(dout, again, "gelu")
     # from x and from tensors alone the default z is activation_checkpoint's
     _, c = ga.activation_checkpoint(x, "gelu_sparse")
-    assert torch.equal(ga.activation_backward(dout, ga.Checkpoint(*c[:3]), "gelu_sparse"),
+    assert torch.equal(ga.activation_backward(dout, ga.Checkpoint(*c), "gelu_sparse"),
                        ga.activation_backward(dout, c, "gelu_sparse"))
     assert torch.equal(ga.activation_backward(dout, x, "gelu_sparse"),
                        ga.activation_backward(dout, x, "gelu_sparse", z=ga.Z_SPARSITY_095))
