@@ -19,10 +19,12 @@
 // every workgroup leaves its sums and one workgroup adds them in order.
 // Integer counts and a fixed order of the fp32 sums: the same bits every time.
 //
-// Measured (kernel trace): 16384 tokens of 128 experts, top 8, bf16 (13 MB): sums
-// 6.9 us, finish 5.0 us, gradient 4.4 us; 64 tokens of 8 experts 4.6 us and
-// 1.9 us.  Latency throughout: a launch, one or two dependent rounds of loads,
-// a finishing workgroup that reads 131 KB by itself.
+// Measured (medians of a kernel trace): 16384 tokens of 128 experts, top 8, bf16
+// (13 MB): sums 7.2 us, finish 5.4 us, gradient 4.7 us; 64 tokens of 8 experts
+// 5.0 us and 2.2 us; 65536 tokens of 128, masked: sums 19.2 us (21 MB), finish 5.0 us,
+// gradient 9.8 us (34 MB).  Latency at the smaller sizes: a launch, one or two
+// dependent rounds of loads, a finishing workgroup that reads 131 KB by itself; at
+// the larger ones the sums run on half of the compute units.
 #include "ga_internal.h"
 #include "ga_train.h"
 
@@ -431,7 +433,8 @@ hipError_t gradient_dt(const Gradient &a) {
 // One workgroup up to 2^15 logits (its launch alone is then most of the time);
 // past that a workgroup for every 2^14, on at most half of the compute units:
 // the one that finishes reads 8 E bytes of each (16384 tokens of 128 experts,
-// bf16: 7.0 us and 4.9 us to finish, 6.6 us and 7.0 us with 256 workgroups).
+// bf16, fastest of a trace: 7.0 us and 4.9 us to finish, 6.6 us and 7.0 us with 256
+// workgroups).
 int balance_groups(int64_t rows, int64_t experts, int cus) {
     const int64_t n = rows * experts, most = cus > 1 ? cus / 2 : 1;
     if (n <= 1 << 15) return 1;

@@ -15,12 +15,14 @@
 // column.  The live count is read on the device and the grid comes from the
 // capacity alone, as in the forward-only kernels.
 //
-// Measured (kernel trace, bf16): silu forward with codes, 12288 live rows of
-// 768 (76 MB) 14.0 us, 5.4 TB/s, its backward from codes 13.2 us, 5.8 TB/s;
-// gelu (erf) forward 8192 x 4096 (272 MB) 45 us, 6.0 TB/s, backward 42.7 us,
-// 6.4 TB/s; store 4096 x 16384 (203 MB) 31.8 us, 6.4 TB/s, restore 33.2 us,
-// 6.1 TB/s; gelu backward from x, 1023 x 4099 fp16 (42 MB, rows off 16-byte
-// alignment) 8.7 us, 4.8 TB/s.
+// Measured (medians of a kernel trace, bf16 unless said): silu forward with codes,
+// 12288 live rows of 768 (76 MB) 16.6 us, 4.6 TB/s, its backward from codes
+// 14.8 us, 5.1 TB/s; forward and backward of 8192 x 4096 (271 MB each) gelu, erf
+// 46.2 and 43.4 us, tanh 45.8 and 43.7 us (5.9 and 6.2 TB/s), squared ReLU (169 MB)
+// 30.8 and 27.6 us, 5.5 and 6.1 TB/s, in fp32 (472 MB) silu 88.8 and 87.0 us, gelu
+// (erf) 89.8 and 88.2 us, 5.3 TB/s; store 4096 x 16384 (203 MB) 34.0 us, 6.0 TB/s,
+// restore 34.6 us, 5.9 TB/s; gelu backward from x, 1023 x 4099 fp16 (42 MB, rows off
+// 16-byte alignment) 10.4 us, 4.0 TB/s.
 #include "ga_internal.h"
 #include "ga_train.h"
 
@@ -33,9 +35,9 @@ constexpr uint32_t FLAT_GROUPS = FLAT_BLOCK / 16;
 constexpr int OP_NONE = -1;
 
 // Blocks a 16-lane group has in flight.  Two where a block is one 16-byte load
-// a lane (4096 rows of 16384, bf16: store 31.8 us, 36.3 with one, 32.4 with
-// four); one where it is more (gelu forward, 8192 rows of 4096, bf16: 44.0 us,
-// 47.2 with two).
+// a lane (4096 rows of 16384, bf16, fastest of a trace: store 31.8 us, 36.3 with
+// one, 32.4 with four); one where it is more (gelu forward, 8192 rows of 4096,
+// bf16: 44.0 us, 47.2 with two).
 template <int DT> constexpr int unroll_of(int halves) { return DT != DT_F32 && halves == 1 ? 2 : 1; }
 
 template <int ACT>

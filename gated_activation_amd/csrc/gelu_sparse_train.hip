@@ -17,7 +17,7 @@
 //
 // gelu_tanh'(0) is 1/2, so the gradient jumps where the gate passes the
 // cutoff: the side is decided from sums in fp64, which runs at fp32's rate here
-// (34 T lane operations a second either way).  The kept codes are those of t, with t > 0 never below
+// (34 T lane operations a second either way), of differences in fp64.  The kept codes are those of t, with t > 0 never below
 // code 1: an 8-bit gate would change sides within half a step of the cutoff.
 // What the codes are relative to is kept as two floats a row, (c, s).
 //
@@ -26,13 +26,14 @@
 // of squares, see shifted_moments), one for G.  dup goes out as soon as it is
 // formed; only q and t stay for the second half.
 //
-// Measured (kernel trace, bf16): forward 2048 x 16384 (272 MB) 50.5 us,
-// 5.4 TB/s, its vector units busy 74 % of the time (about 44 instructions a
-// value, half of them for the two codes); backward from codes 48.5 us,
-// 5.6 TB/s; backward from x 2048 x 8192 (168 MB) 28.8 us, 5.8 TB/s, 2048 x 16384
-// 59 us, 5.7 TB/s; forward 16384 x 2048 46.5 us, backward from codes 44.4 us,
-// 6.1 TB/s.  At d = 65536 some registers spill: forward 512 rows 75 us, backward
-// from codes 53 us, from x 77 us.
+// Measured (medians of a kernel trace, bf16): forward 2048 x 16384 (271 MB)
+// 52 - 55 us, 4.9 - 5.2 TB/s, its vector units busy 74 % of the time (about 44
+// instructions a value, half of them for the two codes); backward from codes
+// 51.4 us, 5.3 TB/s; backward from x 2048 x 8192 (168 MB) 32.0 us, 5.2 TB/s,
+// 2048 x 16384 (336 MB) 61.7 us, 5.4 TB/s; forward 16384 x 2048 48.2 us, 5.6 TB/s,
+// backward from codes 45.1 us, 6.0 TB/s; 512 x 65536 forward 57.9 us, backward from
+// codes 52.6 us, from x 75.4 us, where eight octets a lane spill (in both backward
+// forms, and in fp32's forward).
 #include "ga_internal.h"
 #include "ga_train.h"
 
@@ -323,7 +324,7 @@ hipError_t launch_dt(const Args &a) {
     }
     // From x at 16 waves of two octets the backward needs more than the 64
     // registers that let two workgroups share a compute unit: 2048 rows of
-    // 16384, bf16, 69 us, against 59 us for eight waves of four.
+    // 16384, bf16, 69 us, against 59 us for eight waves of four (fastest of a trace).
     constexpr int W = P == BACKWARD ? 8 : 16;
     if (a.d <= 16384) return launch_as<P, DT, W, 32 / W>(a);
     if (a.d <= 32768) return launch_as<P, DT, 16, 4>(a);

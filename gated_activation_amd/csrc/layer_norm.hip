@@ -26,13 +26,14 @@
 // launch adds the workgroups' partials, again in a fixed order, so the result
 // does not depend on scheduling.  One workgroup per compute unit keeps those
 // partials at 8 d bytes times 256 (two per compute unit: 8192 x 4096 from codes
-// 39.9 us, 33.6 us with one).
+// 39.9 us, 33.6 us with one, fastest of a trace).
 //
-// Measured (kernel trace): forward 16384 x 2048 bf16 (134 MB) 22.4 - 24 us,
-// 5.6 - 6.0 TB/s; with codes 8192 x 4096 (170 MB) 32.8 us, 5.2 TB/s; backward from
-// codes 33.3 us and 4 us for the sums (170 MB, 4.5 TB/s); backward from x,
-// 4096 x 4096 fp32 (201 MB) 39.6 us and 4.7 us, 4.5 TB/s; 4001 x 1027 fp32 (49 MB)
-// 15.1 us and 2.8 us, most of it the first rows' and the sums' latency.
+// Measured (medians of a kernel trace): forward 16384 x 2048 bf16 (134 MB) 25.1 us,
+// 5.4 TB/s; with codes 8192 x 4096 (169 MB) 35.4 us, 4.8 TB/s; backward from codes
+// 33.9 us and 4.6 us for the sums (169 MB, 4.4 TB/s); backward from x, 4096 x 4096
+// fp32 (201 MB) 42.4 us and 4.7 us, 4.3 TB/s; 4001 x 1027 fp32 (49 MB) 16.3 us and
+// 4.0 us: 1027 columns are 129 octets on a team of 256 lanes, the lanes past them
+// load and store the row's last octet again, and the sums' launch is latency.
 #include <type_traits>
 
 #include "ga_internal.h"
@@ -49,7 +50,7 @@ template <int DT, bool WIDE> constexpr int weight_type() { return WIDE ? DT_F32 
 // halve what the row's reductions cost a value; a row of up to 1024 values is
 // a wavefront's own and needs no barrier.  Four octets a lane for the forward
 // took 34.7 us for 38.2 at 4096 x 8192 bf16 with codes, but 35.4 for 34.3 at
-// 4096 columns, 33.6 for 32.9 at 2048, and 3.0 for 2.4 for a single row.
+// 4096 columns, 33.6 for 32.9 at 2048, and 3.0 for 2.4 for a single row (medians).
 template <int LANES_, int V_, bool TINY_ = false> struct Team {
     static constexpr int LANES = LANES_, V = V_;
     static constexpr bool TINY = TINY_;  // rows of fewer than eight values
@@ -166,8 +167,8 @@ __global__ __launch_bounds__(forward_block<T::LANES>()) void forward_kernel(
 constexpr int BACK_BLOCK = 512;
 
 // fp32 rows up to 4096 values: one octet a lane, which leaves the registers to
-// load a row ahead (4001 rows of 1027: 15.3 us, 17.8 us with two octets and
-// none ahead).
+// load a row ahead (4001 rows of 1027, fastest of a trace: 15.3 us, 17.8 us with two
+// octets and none ahead).
 template <bool F32, typename F>
 auto by_width_backward(int64_t d, F &&f) {
     constexpr int V = F32 ? 1 : 2;
@@ -184,8 +185,8 @@ auto by_width_backward(int64_t d, F &&f) {
 // read twice.  SUMS leaves each 8192-column strip's part of a row's sums in
 // the workspace; APPLY adds a row's parts and does the rest for strips of 1024
 // columns, a wavefront to a row, so that a workgroup adds up eight rows and few
-// partials are left.  (Four and eight octets a lane, one pass, spilled: 2048
-// rows of 16384, bf16 from codes, took 80 us, 1024 rows of 32768 414 us, against
+// partials are left.  (Fastest of a trace: four and eight octets a lane, one pass,
+// spilled: 2048 rows of 16384, bf16 from codes, took 80 us, 1024 rows of 32768 414 us, against
 // 52 us either way; APPLY in strips of 8192 columns took 33 us for 311 rows of
 // 20897, from x, against 23 us.)
 enum Stage { WHOLE, SUMS, APPLY };

@@ -330,7 +330,8 @@ ga_status ga_gelu_and_mul_sparse_down_with_plan(const void *gu, const void *w, v
  *     code  = 127 x / m, the exact quotient rounded to the nearest integer
  *             (ties to even), an int8 in [-127, 127]
  *     scale = m / 127 in fp32
- *     value = code * scale, within m / 254 of x (up to fp32 rounding)
+ *     value = code * scale, within m / 254 of x (up to fp32 rounding; a positive
+ *             gate - cutoff below m / 254 has code 1: within m / 127)
  * (A 16-bit row's differences from its own mean or cutoff are coded from the
  * fp32 quotient: one within 127 * 2^-21 of a half-integer may go to either side.)
  * A block that holds a NaN, an infinity or a magnitude of 2^126 or more has
