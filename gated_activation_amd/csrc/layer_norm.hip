@@ -202,7 +202,7 @@ inline bool in_strips(int64_t d) { return strips_of<SumsTeam>(d) > 1; }
 template <int DT, int V> constexpr int rows_ahead() { return V * (DT == DT_F32 ? 2 : 1) <= 2 ? 1 : 0; }
 
 // The row's mean less the fp32 m it came as, from the sum of x - m.  Taken where
-// |m| r > 4, with n off by 2^-22 otherwise, which is of the order of the other
+// |m| r > 4, with n off by at most 2^-22 otherwise, of the order of the other
 // roundings of n; a sum of more than m's rounding can leave (and a few roundings
 // of a mean that was itself summed in fp32) means that m is not meant to be the
 // row's mean, and m is used as it is.
