@@ -27,6 +27,19 @@ Training (no autograd graph: each backward is its own call):
     layer_norm_backward(dy, kept, weight, stats) -> dx, dweight, dbias
     balance_loss(logits, experts)               -> Balance (loss, counts, offsets, tokens)
     balance_loss_backward(logits, balance, dloss) -> dlogits
+
+The feed-forward layer, its products and the activation (bf16 / fp16):
+
+    feed_forward(x, w_in, w_down, activation)         -> y = (act(gate) * up) w_down^T
+    feed_forward_train(x, w_in, w_down, activation)   -> y, kept (gate | up)
+    feed_forward_backward(dy, x, kept, w_in, w_down, activation) -> dx, dw_in, dw_down
+
+and in microscaled 4 bits (Mxfp4: codes, scales, d):
+
+    mxfp4_quantize(x), mxfp4_dequantize(q, dtype)
+    activation_mxfp4(x, activation)                   -> Mxfp4 of the activation's result
+    mxfp4_product(a, w, dtype)                        -> a w^T
+    feed_forward_mxfp4(x, w_in, w_down, activation)   -> y
 """
 from ._lib import (  # noqa: F401
     GA_BF16, GA_F16, GA_F32, GA_OK, GA_EINVAL, GA_EUNSUPPORTED, GA_EHIP, GA_MAX_D, GA_ROUND_INTERMEDIATES,
@@ -45,4 +58,9 @@ from ._train import (  # noqa: F401
     checkpoint_store, checkpoint_restore, activation_checkpoint, activation_backward,
     layer_norm, layer_norm_checkpoint, layer_norm_backward, layer_norm_backward_workspace_bytes,
     balance_loss, balance_loss_backward, balance_loss_workspace_bytes,
+)
+from ._feed_forward import (  # noqa: F401
+    GA_MXFP4_BLOCK, Mxfp4, feed_forward, feed_forward_train, feed_forward_backward, feed_forward_workspace_bytes,
+    feed_forward_backward_workspace_bytes, mxfp4_quantize, mxfp4_dequantize, activation_mxfp4, mxfp4_product,
+    mxfp4_product_workspace_bytes, feed_forward_mxfp4, feed_forward_mxfp4_workspace_bytes,
 )

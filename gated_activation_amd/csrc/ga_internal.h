@@ -190,4 +190,56 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
                                    int32_t rows, int32_t experts, int32_t k, float coefficient, const int32_t *live,
                                    int cus, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// The feed-forward layer's products, 16-bit and microscaled 4-bit operands
+// (ga_tile.h, ga_mx.h).
+// ---------------------------------------------------------------------------
+// Tile and slices of one product of F features, T tokens and K values: tiles of
+// 256 or 128 features (half as many where a gate and an up half share a tile)
+// and tokens, k in `splits` slices of k_split values whose partial sums a second
+// launch adds (splits * T * F fp32, twice that with two halves).
+enum : int { PRODUCT_BIG, PRODUCT_MID };
+struct ProductPlan {
+    int tile, splits;
+    int32_t k_split;
+    int64_t workgroups;
+    size_t partial_bytes;
+};
+// step: values of k a step (64 of 16 bits, 256 of 4)
+ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int step);
+
+// Bytes of workspace, and where its parts begin.
+struct FeedForwardSpace {
+    size_t hidden, gradient, partial, total;
+};
+FeedForwardSpace feed_forward_space(int64_t rows, int64_t H, int64_t d, int halves);
+FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d, int halves);
+
+// op: OP_* above; kept may be null.
+hipError_t launch_feed_forward(int dtype, int op, const void *x, const void *w_in, const void *w_down, void *y, void *kept,
+                               int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                               hipStream_t stream);
+hipError_t launch_feed_forward_backward(int dtype, int op, const void *dy, const void *x, const void *kept,
+                                        const void *w_in, const void *w_down, void *dx, void *dw_in, void *dw_down,
+                                        int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                                        hipStream_t stream);
+
+// op: OP_*, or -1 for x itself.
+hipError_t launch_mxfp4_quantize(int dtype, int op, const void *in, void *codes, uint8_t *scales, int32_t rows,
+                                 uint32_t d, const int32_t *live, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(int dtype, const void *codes, const uint8_t *scales, void *out, int32_t rows,
+                                   uint32_t d, const int32_t *live, hipStream_t stream);
+// out [rows, n] of `dtype` from a [rows, k] and w [n, k].
+size_t mxfp4_product_space(int64_t rows, int64_t n, int64_t k);
+hipError_t launch_mxfp4_product(int dtype, const void *a, const uint8_t *a_scales, const void *w, const uint8_t *w_scales,
+                                void *out, int32_t rows, int32_t n, int32_t k, const int32_t *live, uint8_t *workspace,
+                                hipStream_t stream);
+struct FeedForward4Space {
+    size_t x_codes, x_scales, h_codes, h_scales, partial, total;
+};
+FeedForward4Space feed_forward_mxfp4_space(int64_t rows, int64_t H, int64_t d, int halves);
+hipError_t launch_feed_forward_mxfp4(int dtype, int op, const void *x, const void *w_in, const uint8_t *w_in_scales,
+                                     const void *w_down, const uint8_t *w_down_scales, void *y, int32_t rows, int32_t H,
+                                     int32_t d, const int32_t *live, uint8_t *workspace, hipStream_t stream);
+
 }  // namespace ga

@@ -1,0 +1,612 @@
+// The tiled matrix product of the feed-forward layer (gfx950): device code
+// shared by the 16-bit and the microscaled 4-bit kernels.
+//
+//   D[f, t] = sum over k of A[f, k] B[t, k]      f: features, t: tokens
+//
+// in fp32 on the matrix cores, then an epilogue.  Each operand is stored either
+// with k contiguous (a row of A or B per feature or token) or with k strided (a
+// row per k): a weight gradient sums over tokens, so both its operands are.
+//
+// A workgroup owns FT features x TT tokens, its WF x WT wavefronts NF x NT
+// fragments of 16 x 16 each.  Per step 128 bytes of k (64 values of 16 bits, 256
+// of 4) of both tiles are brought into LDS by loads that write LDS themselves,
+// into the half that the step before last used, while the matrix cores work on
+// the other half: one barrier a step.
+//
+// Bounds.  Every load goes through a buffer descriptor that ends with the
+// operand's last row (the last live token's, where tokens are bounded), so what
+// lies past it reads as zero and adds nothing; a k past the end of a contiguous
+// row is given an offset past the descriptor's end.  Columns past the last
+// feature or token of a strided operand read the next row: they reach only
+// elements of D that are not stored.
+//
+// LDS layout.  The loads write 16-byte chunks in lane order, so the order in
+// LDS is chosen by which chunk each lane asks for.  A row of a contiguous
+// operand is eight chunks; chunk c of row r sits in slot c ^ (r >> 1 & 7), and
+// the 16 rows that 16 lanes read at one c then cover all 64 banks.  A row of a
+// strided operand is FT (TT) values; ds_read_b64_tr_b16 hands each lane four
+// k of its own column from four rows, and chunks are moved by swizzle_a / _b of
+// the row so that the 16 pieces of a read lie in different banks.
+//
+// Which feature a row of the MFMA holds is free: row m of fragment j is feature
+// (m / 4) 4 NF + 4 j + m % 4 of the wavefront's 16 NF.  A lane's NF results of
+// four rows are then 4 NF consecutive features of one token, 16-byte stores.
+// With a gate and an up half fragments j < NF / 2 are gate and the others up of
+// the same features, so one lane holds both.
+#pragma once
+
+#include "ga_internal.h"
+#include "ga_mx.h"
+#include "ga_train.h"
+
+namespace ga {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+enum : int { DT_MX4 = 3 };  // operands of 4 bits with scales; the results have a type of their own
+enum Epilogue : int { EPI_STORE, EPI_GATED, EPI_BACKWARD, EPI_QUANTIZE, EPI_PARTIAL };
+
+constexpr int STEP_BYTES = 128;  // bytes of k a row and step
+constexpr uint32_t FAR = 0x80000000u;  // past the end of every descriptor
+
+// What a product reads and writes.  Rows are in bytes.
+struct TileArgs {
+    const void *a, *b;
+    const uint8_t *a_scales, *b_scales;  // MX4: [rows, blocks]
+    int64_t a_row, b_row;
+    int32_t F, T, K;                     // K: values; strided operands: rows
+    int32_t blocks;                      // MX4: blocks of 32 a row
+    const int32_t *live;                 // bounds T, or K where both operands are strided
+    int32_t splits, k_split;             // slices of k (values, a multiple of the step)
+    float *partial;                      // EPI_PARTIAL: [splits, T, gated ? 2 F : F]
+    void *out;                           // STORE y [T, F]; GATED h [T, F]; BACKWARD dz; QUANTIZE codes
+    void *out2;                          // GATED z [T, 2 F] or null; BACKWARD h [T, F]; QUANTIZE scales
+    const void *z;                       // BACKWARD: gate | up [T, 2 F]
+};
+
+template <int DT> struct KPerStep { static constexpr int value = DT == DT_MX4 ? 256 : 64; };
+
+// ---------------------------------------------------------------------------
+// Epilogues of eight consecutive features f .. f + 7 of token t (F is a multiple
+// of eight, so they are all there or none is).
+// ---------------------------------------------------------------------------
+template <int ACT> constexpr bool act_gated() { return ACT != OP_SQUARED_RELU; }
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float x) {
+    if constexpr (ACT == OP_SILU_MUL) return silu(x);
+    else if constexpr (ACT == OP_GELU_TANH_MUL) return gelu_tanh(x);
+    else if constexpr (ACT == OP_GELU_ERF_MUL) return gelu_erf(x);
+    else {
+        const float r = __builtin_fmaxf(x, 0.0f);
+        return r * r;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void slope_of(float x, float &f, float &df) {
+    if constexpr (ACT == OP_SILU_MUL) silu_slope(x, f, df);
+    else if constexpr (ACT == OP_GELU_TANH_MUL) gelu_tanh_slope(x, f, df);
+    else if constexpr (ACT == OP_GELU_ERF_MUL) gelu_erf_slope(x, f, df);
+    else {
+        const float r = __builtin_fmaxf(x, 0.0f);
+        f = r * r;
+        df = 2.0f * r;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[8]) {
+    oct_store<DT, false>((typename Elem<DT>::storage *)base + at, v, 8);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void *base, int64_t at, float (&v)[8]) {
+    Oct<DT> o;
+    oct_load<DT, false>(o, (const typename Elem<DT>::storage *)base + at, 8);
+    oct_unpack<DT>(o, v);
+}
+
+// act(gate) * up (or act(gate)) of eight features.
+template <int ACT>
+__device__ __forceinline__ void activate8(const float (&g)[8], const float (&u)[8], float (&h)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = act_gated<ACT>() ? act_of<ACT>(g[e]) * u[e] : act_of<ACT>(g[e]);
+}
+
+template <int DT, int ACT>
+__device__ __forceinline__ void gated8(const TileArgs &p, int64_t t, int32_t f, const float (&g)[8], const float (&u)[8]) {
+    constexpr bool GATED = act_gated<ACT>();
+    const int64_t F = p.F;
+    if (p.out2 != nullptr) {
+        store8<DT>(p.out2, t * (GATED ? 2 * F : F) + f, g);
+        if constexpr (GATED) store8<DT>(p.out2, t * 2 * F + F + f, u);
+    }
+    float h[8];
+    activate8<ACT>(g, u, h);
+    store8<DT>(p.out, t * F + f, h);
+}
+
+template <int DT, int ACT>
+__device__ __forceinline__ void backward8(const TileArgs &p, int64_t t, int32_t f, const float (&dh)[8]) {
+    constexpr bool GATED = act_gated<ACT>();
+    const int64_t F = p.F, at = t * (GATED ? 2 * F : F) + f;
+    float g[8], u[8], h[8], dg[8], du[8];
+    load8<DT>(p.z, at, g);
+    if constexpr (GATED) load8<DT>(p.z, at + F, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float v, dv;
+        slope_of<ACT>(g[e], v, dv);
+        if constexpr (GATED) {
+            h[e] = v * u[e];
+            dg[e] = dh[e] * u[e] * dv;
+            du[e] = dh[e] * v;
+        } else {
+            h[e] = v;
+            dg[e] = dh[e] * dv;
+        }
+    }
+    store8<DT>(p.out, at, dg);
+    if constexpr (GATED) store8<DT>(p.out, at + F, du);
+    store8<DT>(p.out2, t * F + f, h);
+}
+
+// Features f .. f + 7 of a row of any length.
+template <int DT>
+__device__ __forceinline__ void store_row(const TileArgs &p, int64_t t, int32_t f, const float (&v)[8]) {
+    oct_store<DT, false>((typename Elem<DT>::storage *)p.out + t * p.F + f, v, p.F - f);
+}
+
+__device__ __forceinline__ uint32_t top8(const float (&h)[8]) {
+    uint32_t top = magnitude(h[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = max(top, magnitude(h[e]));
+    return top;
+}
+
+// What an epilogue does with eight features of a token (in: they are there).
+// QUANTIZE: F is a multiple of 32, and the four lanes of a quad hold a block of it.
+template <int EPI, int ACT, int OUT>
+__device__ __forceinline__ void finish8(const TileArgs &p, int64_t t, int32_t f, bool in, const float (&v)[8],
+                                        const float (&u)[8]) {
+    if constexpr (EPI == EPI_QUANTIZE) {
+        float h[8];
+        activate8<ACT>(v, u, h);
+        uint32_t top = top8(h);
+        top = dpp_umax<0xB1>(top);
+        top = dpp_umax<0x4E>(top);
+        if (in) {
+            const uint32_t s = mx_scale_byte(top);
+            const int64_t block = t * (p.F / MX_BLOCK) + f / MX_BLOCK;
+            ((uint32_t *)p.out)[block * 4 + f / 8 % 4] = mx_codes8(h, s);
+            if (f % MX_BLOCK == 0) ((uint8_t *)p.out2)[block] = (uint8_t)s;
+        }
+    } else if (in) {
+        if constexpr (EPI == EPI_STORE) store_row<OUT>(p, t, f, v);
+        else if constexpr (EPI == EPI_GATED) gated8<OUT, ACT>(p, t, f, v, u);
+        else backward8<OUT, ACT>(p, t, f, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The workgroup's tile: the tiles are dealt to the eight XCDs in contiguous runs
+// (workgroups go to them in turn), and a run walks panels of PANEL token tiles,
+// so the workgroups that share an L2 share their operands' rows.
+// ---------------------------------------------------------------------------
+constexpr uint32_t XCDS = 8, PANEL = 8;
+
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t n, uint32_t nf, uint32_t nt, uint32_t &ft, uint32_t &tt) {
+    const uint32_t q = n / XCDS, r = n % XCDS, x = b % XCDS;
+    const uint32_t id = x * q + (x < r ? x : r) + b / XCDS;
+    const uint32_t panel = id / (PANEL * nf), first = panel * PANEL;
+    const uint32_t height = nt - first < PANEL ? nt - first : PANEL, in = id - first * nf;
+    tt = first + in % height;
+    ft = in / height;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, int64_t bytes) {
+    const int64_t n = bytes < 0 ? 0 : bytes > 0x7FFFFFF0 ? 0x7FFFFFF0 : bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)n, 0x00020000);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, void *lds, uint32_t voffset, int soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, voffset, soffset, 0, 0);
+}
+
+// Chunk swizzles of strided operands by k row (see above): a read's four rows k % 4.
+template <int NF>
+__device__ __forceinline__ uint32_t swizzle_a(uint32_t k) {
+    return NF == 8 ? (k & 3) : (k & 1) | (k & 2) << 2;
+}
+__device__ __forceinline__ uint32_t swizzle_b(uint32_t k) { return (k & 3) << 1; }
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(const i32x4 a, const i32x4 b, f32x4 c, int sa, int sb, int kk) {
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else if constexpr (DT == DT_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else {
+        const i32x8 wa = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, wb = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
+        // formats 4: e2m1; byte kk of the scale words
+        if (kk == 0) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, sa, 0, sb);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 1, sa, 1, sb);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel.  AK / BK: the operand is strided.  GATED: A has 2 F rows.
+// ---------------------------------------------------------------------------
+template <int DT_, bool AK_, bool BK_, int WF_, int WT_, int NF_, int NT_> struct Tile {
+    static constexpr int DT = DT_, WF = WF_, WT = WT_, NF = NF_, NT = NT_;
+    static constexpr bool AK = AK_, BK = BK_;
+    static constexpr int W = WF * WT, FT = WF * NF * 16, TT = WT * NT * 16;
+    static constexpr int KS = KPerStep<DT>::value;
+    static constexpr int LA = FT / 8 / W, LB = TT / 8 / W;  // 1024-byte loads a wavefront and step
+    static_assert(LA * 8 * W == FT && LB * 8 * W == TT, "loads");
+    static_assert(DT != DT_MX4 || (!AK && !BK && W * 64 == FT + TT), "one row's scales a thread");
+};
+
+// Eight scales of a row at block b; the row's tail reads as 2^-127 (codes past it are zero).
+__device__ __forceinline__ uint2 scales8(const uint8_t *row, int32_t b, int32_t blocks) {
+    if (b + 8 <= blocks) {
+        const u32x2 v = *reinterpret_cast<const u32x2_a1 *>(row + b);
+        return uint2{v.x, v.y};
+    }
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (b + e < blocks) w[e >> 2] |= (uint32_t)row[b + e] << ((e & 3) * 8);
+    return uint2{w[0], w[1]};
+}
+
+template <typename C, int EPI, int ACT, int OUT>
+__global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
+    constexpr int DT = C::DT, W = C::W, FT = C::FT, TT = C::TT, NF = C::NF, NT = C::NT;
+    constexpr bool MX = DT == DT_MX4;
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE || EPI == EPI_PARTIAL) && act_gated<ACT>() && !C::AK;
+    constexpr int FW = GATED ? FT / 2 : FT;  // features of D a workgroup
+
+    __shared__ __attribute__((aligned(16))) uint8_t a0[FT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t b0[TT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t b1[TT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint2 sc0[MX ? FT + TT : 1];
+    __shared__ __attribute__((aligned(16))) uint2 sc1[MX ? FT + TT : 1];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, wf = wave / C::WT, wt = wave % C::WT;
+    const uint32_t nf = (uint32_t)((p.F + FW - 1) / FW), nt = (uint32_t)((p.T + TT - 1) / TT), n = nf * nt;
+    uint32_t ft, tt;
+    tile_of(blockIdx.x % n, n, nf, nt, ft, tt);
+    const int split = (int)(blockIdx.x / n);
+    const int32_t f0 = (int32_t)(ft * FW), t0 = (int32_t)(tt * TT);
+    int32_t T = p.T, K = p.K;
+    if (p.live != nullptr) {
+        if constexpr (C::BK) K = clamp_live(p.live, K);
+        else T = clamp_live(p.live, T);
+    }
+    if (t0 >= T) return;
+    const int32_t kb = split * p.k_split;
+    const int32_t ke = p.k_split < K - kb ? kb + p.k_split : K;  // past it: zeros (may be below kb)
+    const int32_t steps = ke > kb ? (ke - kb + C::KS - 1) / C::KS : 0;
+
+    // ---- what this lane loads ----
+    uint32_t va[C::LA], vb[C::LB];
+    uint32_t chunk_a[C::LA], chunk_b[C::LB];  // contiguous operands: the chunk of the row's 128 bytes
+#pragma unroll
+    for (int j = 0; j < C::LA; ++j) {
+        const int i = j * W + wave;
+        if constexpr (C::AK) {
+            constexpr int CPR = FT / 8, RPI = 64 / CPR;
+            const uint32_t k = i * RPI + lane / CPR;
+            va[j] = k * (uint32_t)p.a_row + (((lane % CPR) ^ swizzle_a<NF>(k)) * 16);
+        } else {
+            const uint32_t row = i * 8 + (lane >> 3), m = row & 15;
+            chunk_a[j] = (lane & 7) ^ (row >> 1 & 7);
+            uint32_t frag = row / 16 % NF;
+            if constexpr (GATED) {
+                frag %= NF / 2;
+                va[j] = (row / (16 * NF) * (8 * NF) + (m >> 2) * (2 * NF) + frag * 4 + (m & 3)) * (uint32_t)p.a_row;
+            } else {
+                va[j] = (row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3)) * (uint32_t)p.a_row;
+            }
+            va[j] += chunk_a[j] * 16;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < C::LB; ++j) {
+        const int i = j * W + wave;
+        if constexpr (C::BK) {
+            constexpr int CPR = TT / 8, RPI = 64 / CPR;
+            const uint32_t k = i * RPI + lane / CPR;
+            vb[j] = k * (uint32_t)p.b_row + (((lane % CPR) ^ swizzle_b(k)) * 16);
+        } else {
+            const uint32_t row = i * 8 + (lane >> 3);
+            chunk_b[j] = (lane & 7) ^ (row >> 1 & 7);
+            vb[j] = row * (uint32_t)p.b_row + chunk_b[j] * 16;
+        }
+    }
+    const uint8_t *a = (const uint8_t *)p.a, *b = (const uint8_t *)p.b;
+    const int32_t rows_a = p.F - f0 < FW ? p.F - f0 : FW, rows_b = T - t0 < TT ? T - t0 : TT;
+    __amdgpu_buffer_rsrc_t wa = window(a, 0), wu = wa, wb = wa;
+    if constexpr (!C::AK) {
+        wa = window(a + f0 * p.a_row, rows_a * p.a_row);
+        if constexpr (GATED) wu = window(a + ((int64_t)p.F + f0) * p.a_row, rows_a * p.a_row);
+    }
+    if constexpr (!C::BK) wb = window(b + t0 * p.b_row, rows_b * p.b_row);
+
+    // MX4: the row whose scales this thread brings
+    const uint8_t *scale_row = nullptr;
+    if constexpr (MX) {
+        if ((int)threadIdx.x < FT) {
+            const uint32_t row = threadIdx.x, m = row & 15;
+            uint32_t frag = row / 16 % NF, f;
+            bool up = false;
+            if constexpr (GATED) {
+                up = frag >= NF / 2;
+                frag %= NF / 2;
+                f = row / (16 * NF) * (8 * NF) + (m >> 2) * (2 * NF) + frag * 4 + (m & 3);
+            } else {
+                f = row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3);
+            }
+            int64_t at = f0 + f < (uint32_t)p.F ? f0 + f : p.F - 1;  // past the end: any row, not stored
+            if (up) at += p.F;
+            scale_row = p.a_scales + at * p.blocks;
+        } else {
+            const int32_t t = t0 + (int)threadIdx.x - FT;
+            scale_row = p.b_scales + (int64_t)(t < T ? t : T - 1) * p.blocks;
+        }
+    }
+
+    const auto load = [&](int32_t s, uint8_t *la, uint8_t *lb) {
+        const int32_t k0 = kb + s * C::KS;
+        const bool tail = k0 + C::KS > ke;
+        // values of this step that are there; a row of 4-bit codes ends with its last block's 16 bytes
+        const uint32_t chunks = MX ? (uint32_t)((ke - k0 + 31) / 32) : (uint32_t)((ke - k0 + 7) / 8);
+        if constexpr (C::AK)
+            wa = window(a + k0 * p.a_row + (int64_t)f0 * 2, (int64_t)(tail ? ke - k0 : C::KS) * p.a_row - (int64_t)f0 * 2);
+        if constexpr (C::BK)
+            wb = window(b + k0 * p.b_row + (int64_t)t0 * 2, (int64_t)(tail ? ke - k0 : C::KS) * p.b_row - (int64_t)t0 * 2);
+        const int so = MX ? k0 / 2 : k0 * 2;
+#pragma unroll
+        for (int j = 0; j < C::LA; ++j) {
+            uint8_t *at = la + (j * W + wave) * 1024;
+            if constexpr (C::AK) {
+                to_lds(wa, at, va[j], 0);
+            } else {
+                const bool up = GATED && (j * W + wave) / 2 % NF >= NF / 2;
+                to_lds(up ? wu : wa, at, tail && chunk_a[j] >= chunks ? FAR : va[j], so);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < C::LB; ++j) {
+            uint8_t *at = lb + (j * W + wave) * 1024;
+            if constexpr (C::BK) to_lds(wb, at, vb[j], 0);
+            else to_lds(wb, at, tail && chunk_b[j] >= chunks ? FAR : vb[j], so);
+        }
+        // left to itself the compiler moves them down to the wait
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto load_scales = [&](int32_t s) -> uint2 {
+        if constexpr (MX) return scales8(scale_row, (kb + s * C::KS) / 32, ke / 32 + (ke % 32 != 0));
+        return uint2{0, 0};
+    };
+    // bytes 0 4 1 5 | 2 6 3 7: lane group g reads the pair of its two blocks
+    const auto put_scales = [&](uint2 v, uint2 *to) {
+        if constexpr (MX)
+            to[threadIdx.x] = uint2{__builtin_amdgcn_perm(v.y, v.x, 0x05010400u), __builtin_amdgcn_perm(v.y, v.x, 0x07030602u)};
+    };
+
+    // ---- fragments ----
+    f32x4 acc[NF][NT];
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const auto read_row = [&](const uint8_t *tile, int row, int kk) -> i32x4 {
+        return *reinterpret_cast<const i32x4 *>(tile + (row + r) * STEP_BYTES + (((kk * 4 + g) ^ (r >> 1)) * 16));
+    };
+    const auto read_tr = [&](const uint8_t *at) -> i16x4 {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)at);
+    };
+    const int q = r & 3, kr = r >> 2;
+    const auto compute = [&](const uint8_t *la, const uint8_t *lb, const uint2 *sc) {
+        int sa[NF], sb[NT];
+        if constexpr (MX) {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(sc);
+#pragma unroll
+            for (int i = 0; i < NF; ++i) sa[i] = h[(wf * NF * 16 + i * 16 + r) * 4 + g];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sb[j] = h[(FT + wt * NT * 16 + j * 16 + r) * 4 + g];
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x4 fa[NF], fb[NT];
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                if constexpr (C::AK) {
+                    const uint32_t k = kk * 32 + g * 8 + kr;
+                    const uint32_t chunk = ((wf * NF * 16 + q * NF * 4 + i * 4) / 8) ^ swizzle_a<NF>(kr);
+                    const uint8_t *at = la + k * (FT * 2) + chunk * 16 + (i & 1) * 8;
+                    const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * FT * 2);
+                    fa[i] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                } else {
+                    fa[i] = read_row(la, wf * NF * 16 + i * 16, kk);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (C::BK) {
+                    const uint32_t k = kk * 32 + g * 8 + kr;
+                    const uint32_t chunk = ((wt * NT + j) * 2 + (q >> 1)) ^ swizzle_b(kr);
+                    const uint8_t *at = lb + k * (TT * 2) + chunk * 16 + (q & 1) * 8;
+                    const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * TT * 2);
+                    fb[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                } else {
+                    fb[j] = read_row(lb, wt * NT * 16 + j * 16, kk);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j], MX ? sa[i] : 0, MX ? sb[j] : 0, kk);
+        }
+    };
+
+    const auto landed = [] {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        __syncthreads();
+    };
+    if (steps > 0) {
+        load(0, a0, b0);
+        put_scales(load_scales(0), sc0);
+        landed();
+    }
+    uint2 next{};
+    for (int32_t s = 0; s + 2 <= steps; s += 2) {
+        load(s + 1, a1, b1);
+        next = load_scales(s + 1);
+        compute(a0, b0, sc0);
+        put_scales(next, sc1);
+        landed();
+        if (s + 2 < steps) {
+            load(s + 2, a0, b0);
+            next = load_scales(s + 2);
+        }
+        compute(a1, b1, sc1);
+        put_scales(next, sc0);
+        landed();
+    }
+    if (steps & 1) compute(a0, b0, sc0);
+
+    // ---- epilogue ----
+    // Through LDS, 16 KB a wavefront and JT x 16 tokens at a time, so that a lane
+    // ends up with eight consecutive features and neighbouring lanes with the
+    // next ones.  (Straight from the accumulators the unrolled epilogue spills.)
+    // Four results of a lane are 16 bytes of a token's row; chunk c of token t
+    // sits in c ^ t % 16, so that 16 tokens' writes fall into all banks.
+    constexpr int JT = 16 * 1024 / (NF * 16 * 16 * 4), CHUNKS = NF * 4;  // chunks a token
+    static_assert(NT % JT == 0 && FT * STEP_BYTES >= 16 * 1024 && W * 16 * 1024 == 2 * (FT + TT) * STEP_BYTES, "16 KB a wavefront");
+    constexpr int PER = FT * STEP_BYTES / (16 * 1024);  // wavefronts an array
+    uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == 1 ? b0 : wave / PER == 2 ? a1 : b1) + wave % PER * (16 * 1024);
+    constexpr int LANES = CHUNKS / (GATED ? 4 : 2), TOKENS = 64 / LANES;  // lanes a token, tokens a pass
+    const int oct = lane % LANES;
+    const int32_t f = f0 + wf * (LANES * 8) + oct * 8;
+    __syncthreads();
+#pragma unroll
+    for (int half = 0; half < NT / JT; ++half) {
+#pragma unroll
+        for (int jj = 0; jj < JT; ++jj) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                constexpr int HF = NF / 2;
+                const int chunk = GATED ? (i < HF ? g * HF + i : CHUNKS / 2 + g * HF + i - HF) : g * NF + i;
+                *reinterpret_cast<f32x4 *>(mine + ((jj * 16 + r) * CHUNKS + (chunk ^ r)) * 16) = acc[i][half * JT + jj];
+            }
+        }
+#pragma unroll 1
+        for (int pass = 0; pass < JT * 16 / TOKENS; ++pass) {
+            const int tok = pass * TOKENS + lane / LANES;
+            const auto get = [&](int chunk, float (&v)[8]) {
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + (chunk ^ (tok & 15))) * 16);
+                const f32x4 hi = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + ((chunk + 1) ^ (tok & 15))) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+            };
+            float v[8], u[8] = {};
+            get(2 * oct, v);
+            if constexpr (GATED) get(CHUNKS / 2 + 2 * oct, u);
+            const int32_t t = t0 + (wt * NT + half * JT) * 16 + tok;
+            if constexpr (EPI == EPI_PARTIAL) {
+                if (t < T && f < p.F) {
+                    uint32_t *at = (uint32_t *)p.partial + ((int64_t)split * p.T + t) * (GATED ? 2 : 1) * p.F + f;
+                    oct_store<DT_F32, false>(at, v, p.F - f);
+                    if constexpr (GATED) oct_store<DT_F32, false>(at + p.F, u, p.F - f);
+                }
+            } else {
+                finish8<EPI, ACT, OUT>(p, t, f, t < T && f < p.F, v, u);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The epilogue of a product whose k was cut into slices: adds the slices'
+// partial sums in their order.  Eight features of a token a thread.
+// ---------------------------------------------------------------------------
+constexpr int FINISH_BLOCK = 256;
+
+template <int EPI, int ACT, int OUT>
+__global__ __launch_bounds__(FINISH_BLOCK) void finish_kernel(TileArgs p, bool bound_tokens) {
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
+    const int32_t octs = (p.F + 7) / 8;
+    const int32_t T = bound_tokens && p.live != nullptr ? clamp_live(p.live, p.T) : p.T;
+    const int64_t i = (int64_t)blockIdx.x * FINISH_BLOCK + threadIdx.x;
+    const int64_t t = i / octs;
+    const int32_t f = (int32_t)(i - t * octs) * 8;
+    float v[8] = {}, u[8] = {};
+    if (t < T) {
+        const int64_t row = GATED ? 2 * (int64_t)p.F : p.F;
+        const uint32_t *at = (const uint32_t *)p.partial + t * row + f;
+        for (int s = 0; s < p.splits; ++s, at += (int64_t)p.T * row) {
+            Oct<DT_F32> o;
+            float w[8];
+            oct_load<DT_F32, false>(o, at, p.F - f);
+            oct_unpack<DT_F32>(o, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+            if constexpr (GATED) {
+                oct_load<DT_F32, false>(o, at + p.F, p.F - f);
+                oct_unpack<DT_F32>(o, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] += w[e];
+            }
+        }
+    }
+    finish8<EPI, ACT, OUT>(p, t, f, t < T, v, u);
+}
+
+// ---------------------------------------------------------------------------
+// Launches.
+// ---------------------------------------------------------------------------
+template <typename C, int EPI, int ACT, int OUT>
+hipError_t launch_tile(const TileArgs &p, bool halves, hipStream_t stream) {
+    const int64_t fw = halves ? C::FT / 2 : C::FT;
+    const int64_t n = ((p.F + fw - 1) / fw) * (((int64_t)p.T + C::TT - 1) / C::TT) * p.splits;
+    return launch_kernel(tile_kernel<C, EPI, ACT, OUT>, dim3((uint32_t)n), dim3(C::W * 64), stream, p);
+}
+
+template <int EPI, int ACT, int OUT>
+hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t stream) {
+    const int64_t n = ((int64_t)p.T * ((p.F + 7) / 8) + FINISH_BLOCK - 1) / FINISH_BLOCK;
+    return launch_kernel(finish_kernel<EPI, ACT, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
+}
+
+// One product with the planner's tile and slices (plan_product, ga_internal.h).
+template <typename Big, typename Mid, int EPI, int ACT, int OUT>
+hipError_t launch_product(TileArgs p, const ProductPlan &plan, bool halves, float *partial, hipStream_t stream) {
+    p.splits = plan.splits;
+    p.k_split = plan.k_split;
+    p.partial = partial;
+    const bool big = plan.tile == PRODUCT_BIG;
+    if (plan.splits == 1)
+        return big ? launch_tile<Big, EPI, ACT, OUT>(p, halves, stream) : launch_tile<Mid, EPI, ACT, OUT>(p, halves, stream);
+    // the slices' sums: with two halves only for the epilogues that join them
+    constexpr bool JOINS = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
+    constexpr int PART_ACT = JOINS ? OP_SILU_MUL : OP_SQUARED_RELU;
+    const hipError_t e = big ? launch_tile<Big, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream)
+                             : launch_tile<Mid, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream);
+    return e != hipSuccess ? e : launch_finish<EPI, ACT, OUT>(p, !Big::BK, stream);
+}
+
+}  // namespace ga

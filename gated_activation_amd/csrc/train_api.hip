@@ -10,75 +10,15 @@ static_assert(GA_LAYER_NORM_MAX_D == ga::LN_MAX_D && GA_BALANCE_MAX_EXPERTS == g
 
 namespace {
 
+using ga::blocks_of;
+using ga::check_blocks;
+using ga::check_items;
+using ga::check_regions;
+using ga::check_sizes;
 using ga::elem_size;
 using ga::fail;
-using ga::overlaps;
-
-// One array of a call, for the checks that all share.
-struct Region {
-    const char *name;
-    const void *at;
-    size_t bytes;
-    size_t align;
-    bool written;
-    bool optional;
-};
-
-// Null, misaligned and overlapping arrays.  Arrays without a byte may be null;
-// one that is written overlaps no other.
-template <int N>
-ga_status check_regions(const char *op, const Region (&r)[N]) {
-    for (int i = 0; i < N; ++i) {
-        if (r[i].at == nullptr) {
-            if (r[i].optional || r[i].bytes == 0) continue;
-            return fail(GA_EINVAL, "%s: null %s", op, r[i].name);
-        }
-        if ((uintptr_t)r[i].at % r[i].align != 0)
-            return fail(GA_EINVAL, "%s: %s is not aligned to %zu bytes", op, r[i].name, r[i].align);
-        for (int j = 0; j < i; ++j) {
-            if (r[j].at == nullptr || !(r[i].written || r[j].written) || r[i].bytes == 0 || r[j].bytes == 0) continue;
-            if (overlaps(r[i].at, r[i].bytes, r[j].at, r[j].bytes))
-                return fail(GA_EINVAL, "%s: %s and %s overlap", op, r[j].name, r[i].name);
-        }
-    }
-    return GA_OK;
-}
-
-ga_status check_sizes(const char *op, int64_t rows, int64_t d, int64_t most_d, int32_t dtype) {
-    if (rows < 0 || rows > INT32_MAX)
-        return fail(GA_EINVAL, "%s: row count %lld out of [0, 2^31)", op, (long long)rows);
-    if (d < 1) return fail(GA_EINVAL, "%s: d = %lld must be >= 1", op, (long long)d);
-    if (elem_size(dtype) == 0) return fail(GA_EINVAL, "%s: unknown dtype %d", op, (int)dtype);
-    if (d > most_d) return fail(GA_EUNSUPPORTED, "%s: d = %lld above %lld", op, (long long)d, (long long)most_d);
-    return GA_OK;
-}
-
-int64_t blocks_of(int64_t d) { return (d + GA_CHECKPOINT_BLOCK - 1) / GA_CHECKPOINT_BLOCK; }
-
-// Elementwise kernels number the blocks of 128 values in 31 bits; the launches
-// of kernels that give a row `lanes` work-items have fewer than 2^32.
-ga_status check_blocks(const char *op, int64_t blocks) {
-    if (blocks > INT32_MAX)
-        return fail(GA_EUNSUPPORTED, "%s: %lld blocks of 128 values in one call (2^31 or more)", op, (long long)blocks);
-    return GA_OK;
-}
-
-ga_status check_items(const char *op, int64_t rows, int64_t lanes) {
-    if (rows * lanes + 1024 > (int64_t)UINT32_MAX)
-        return fail(GA_EUNSUPPORTED, "%s: %lld rows of %lld lanes in one launch (2^32 work-items or more)", op,
-                    (long long)rows, (long long)lanes);
-    return GA_OK;
-}
-
-int op_of(int32_t activation) {
-    switch (activation) {
-    case GA_ACT_SILU: return ga::OP_SILU_MUL;
-    case GA_ACT_GELU_TANH: return ga::OP_GELU_TANH_MUL;
-    case GA_ACT_GELU_ERF: return ga::OP_GELU_ERF_MUL;
-    case GA_ACT_SQUARED_RELU: return ga::OP_SQUARED_RELU;
-    default: return -1;
-    }
-}
+using ga::op_of;
+using ga::Region;
 
 ga_status check_activation(const char *op, int32_t activation, float z) {
     if (activation < GA_ACT_SILU || activation > GA_ACT_GELU_SPARSE)

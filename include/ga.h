@@ -486,6 +486,103 @@ ga_status ga_balance_loss_backward(const void *logits, const uint8_t *mask, cons
                                    const int32_t *live_rows, ga_stream stream);
 
 /*
+ * ---- The feed-forward layer ----
+ *
+ * The products around the gated activations, in 16 bits and in microscaled 4
+ * bits.  They follow the conventions above.  A written array overlaps no other
+ * array of the call (GA_EINVAL).  live_rows bounds the rows (tokens; NULL: all);
+ * rows at or past it are neither read nor written.  Every sum has a fixed order.
+ *
+ * With the activation's GATED form (SILU, GELU_TANH, GELU_ERF; gate rows of w_in
+ * first, then up rows, zd = 2 d) or SQUARED_RELU (not gated, zd = d):
+ *     z = x w_in^T                  gate | up
+ *     h = act(gate) * up            (SQUARED_RELU: max(z, 0)^2)
+ *     y = h w_down^T
+ * GELU_SPARSE is refused (GA_EUNSUPPORTED): its cutoff is a statistic of the whole
+ * row of z (ga_gelu_and_mul_sparse and ga_gelu_and_mul_sparse_down serve it).
+ * Sums are fp32 on the matrix cores.  z is rounded only where it is kept, h once,
+ * y once.
+ *   x       [rows, H], y [rows, H], w_in [zd, H], w_down [H, d] of dtype GA_BF16 or
+ *           GA_F16 (GA_F32: GA_EUNSUPPORTED), 16-byte aligned
+ *   kept    z in dtype [rows, zd], for the backward pass; NULL: not kept
+ *   H, d    8 .. GA_MAX_D, multiples of 8
+ *   rows    0 .. 2^31 - 1; where a launch would have 2^32 work-items or more (about
+ *           2^31 * 128 / max(H, d) rows): GA_EUNSUPPORTED
+ *   workspace  ga_feed_forward_workspace_bytes() bytes, 256-byte aligned, any
+ *           content; calls that share one must not overlap in time.
+ */
+size_t ga_feed_forward_workspace_bytes(int64_t rows, int64_t H, int64_t d, int32_t activation);
+ga_status ga_feed_forward(const void *x, const void *w_in, const void *w_down, void *y, void *kept, int64_t rows,
+                          int64_t H, int64_t d, int32_t dtype, int32_t activation, const int32_t *live_rows,
+                          void *workspace, size_t workspace_bytes, ga_stream stream);
+
+/*
+ * Its backward pass, from dy [rows, H], x and the kept z:
+ *     dh = dy w_down
+ *     dz = dh up act'(gate) | dh act(gate)      (SQUARED_RELU: 2 max(z, 0) dh)
+ *     dx = dz w_in,  dw_in = dz^T x,  dw_down = dy^T h,  h formed again from z
+ * dh stays in fp32; dz and h are rounded to the type once, dx, dw_in and dw_down
+ * once.  The weights' gradients sum over the live rows (none: zero).
+ */
+size_t ga_feed_forward_backward_workspace_bytes(int64_t rows, int64_t H, int64_t d, int32_t activation);
+ga_status ga_feed_forward_backward(const void *dy, const void *x, const void *kept, const void *w_in, const void *w_down,
+                                   void *dx, void *dw_in, void *dw_down, int64_t rows, int64_t H, int64_t d,
+                                   int32_t dtype, int32_t activation, const int32_t *live_rows, void *workspace,
+                                   size_t workspace_bytes, ga_stream stream);
+
+/*
+ * Microscaled 4-bit arrays (OCP MX, MXFP4): a row in blocks of GA_MXFP4_BLOCK = 32
+ * values, the last one shorter, each with one power of two.  With m the block's
+ * largest magnitude:
+ *     scale   byte s, standing for 2^(s - 127): s = max(127 + floor(log2 m) - 2, 0),
+ *             0 for m = 0
+ *     code    x / 2^(s - 127), exactly, rounded to the nearest of 0, 0.5, 1, 1.5, 2,
+ *             3, 4, 6 (ties to the even code), 6 above 6; bit 3 is x's sign
+ * A block that holds a NaN or an infinity has s = 255: it stands for NaNs.
+ *   codes   uint8 [rows, 16 ceil(d / 32)]: value 2 i of a row in the low and 2 i + 1
+ *           in the high half of byte i, past the row's end 0; 16-byte aligned
+ *   scales  uint8 [rows, ceil(d / 32)]
+ * 1 <= d <= GA_MAX_D; rows * ceil(d / 128) < 2^31 (else GA_EUNSUPPORTED).  The
+ * other arrays have any alignment natural to their type.
+ */
+#define GA_MXFP4_BLOCK 32
+ga_status ga_mxfp4_quantize(const void *in, void *codes, uint8_t *scales, int64_t rows, int64_t d, int32_t dtype,
+                            const int32_t *live_rows, ga_stream stream);
+/* out [rows, d] of `dtype`: the values, rounded once. */
+ga_status ga_mxfp4_dequantize(const void *codes, const uint8_t *scales, void *out, int64_t rows, int64_t d,
+                              int32_t dtype, const int32_t *live_rows, ga_stream stream);
+/* A gated activation (GELU_SPARSE: GA_EUNSUPPORTED) of in [rows, 2d] (SQUARED_RELU
+ * [rows, d]), the value that the forward-only entry points store, quantised. */
+ga_status ga_activation_mxfp4(const void *in, void *codes, uint8_t *scales, int64_t rows, int64_t d, int32_t dtype,
+                              int32_t activation, const int32_t *live_rows, ga_stream stream);
+
+/*
+ * The product of two such arrays, out[r, i] = sum over k of a[r, k] w[i, k] in fp32,
+ * rounded once to dtype (any of the three).  A NaN block makes the outputs of its
+ * row NaN.
+ *   a codes, scales of [rows, k]; w of [n, k]; out [rows, n], any alignment natural
+ *   to its type.  1 <= n < 2^31 - 1024, 1 <= k <= GA_MAX_D.
+ *   workspace  ga_mxfp4_product_workspace_bytes() bytes (may be 0), as above.
+ */
+size_t ga_mxfp4_product_workspace_bytes(int64_t rows, int64_t n, int64_t k);
+ga_status ga_mxfp4_product(const void *a_codes, const uint8_t *a_scales, const void *w_codes, const uint8_t *w_scales,
+                           void *out, int64_t rows, int64_t n, int64_t k, int32_t dtype, const int32_t *live_rows,
+                           void *workspace, size_t workspace_bytes, ga_stream stream);
+
+/*
+ * The feed-forward layer on 4-bit operands: x is quantised, z = q(x) w_in^T stays
+ * in fp32, h = act(gate) up is quantised from fp32, y = q(h) w_down^T.  x and y
+ * [rows, H] of dtype GA_BF16 or GA_F16, any alignment natural to the type; w_in
+ * [zd, H] and w_down [H, d] as codes and scales.  8 <= H <= GA_MAX_D, a multiple of
+ * 8; 32 <= d <= GA_MAX_D, a multiple of 32 (gate and up rows keep blocks of h whole).
+ */
+size_t ga_feed_forward_mxfp4_workspace_bytes(int64_t rows, int64_t H, int64_t d, int32_t activation);
+ga_status ga_feed_forward_mxfp4(const void *x, const void *w_in_codes, const uint8_t *w_in_scales,
+                                const void *w_down_codes, const uint8_t *w_down_scales, void *y, int64_t rows, int64_t H,
+                                int64_t d, int32_t dtype, int32_t activation, const int32_t *live_rows, void *workspace,
+                                size_t workspace_bytes, ga_stream stream);
+
+/*
  * Host-only helper: z = Phi^-1(target_sparsity), the cutoff multiplier for
  * a target fraction of zeros (0.95 -> 1.6448536...).  NaN outside (0, 1).
  * Newton's method on the normal CDF, to full double precision.
