@@ -46,8 +46,9 @@ ga_status check_workspace(const char *op, const void *workspace, size_t bytes, s
     return GA_OK;
 }
 
-// One product's launch.
+// One product's launch; rows and features are counted a few tiles past their end in 32 bits.
 ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool halves, int step) {
+    if (T > INT32_MAX - 1024) return fail(GA_EUNSUPPORTED, "%s: %lld rows (at most 2^31 - 1025)", op, (long long)T);
     return check_items(op, ga::plan_product(F, T, K, halves, step).workgroups, kTileThreads);
 }
 

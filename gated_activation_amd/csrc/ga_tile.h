@@ -11,7 +11,7 @@
 // fragments of 16 x 16 each.  Per step 128 bytes of k (64 values of 16 bits, 256
 // of 4) of both tiles are brought into LDS by loads that write LDS themselves,
 // into the half that the step before last used, while the matrix cores work on
-// the other half: one barrier a step.
+// the other half: one barrier a step, in its middle.
 //
 // Bounds.  Every load goes through a buffer descriptor that ends with the
 // operand's last row (the last live token's, where tokens are bounded), so what
@@ -199,7 +199,7 @@ __device__ __forceinline__ void finish8(const TileArgs &p, int64_t t, int32_t f,
 // (workgroups go to them in turn), and a run walks panels of PANEL token tiles,
 // so the workgroups that share an L2 share their operands' rows.
 // ---------------------------------------------------------------------------
-constexpr uint32_t XCDS = 8, PANEL = 8;
+constexpr uint32_t XCDS = 8, PANEL = 4;
 
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t n, uint32_t nf, uint32_t nt, uint32_t &ft, uint32_t &tt) {
     const uint32_t q = n / XCDS, r = n % XCDS, x = b % XCDS;
@@ -228,18 +228,40 @@ __device__ __forceinline__ uint32_t swizzle_a(uint32_t k) {
 }
 __device__ __forceinline__ uint32_t swizzle_b(uint32_t k) { return (k & 3) << 1; }
 
+// c += a b, written as assembly with the sum and the result in one register:
+// left to choose, the compiler moves the large tile's 128 sums about and spills
+// (8192 x 4096 x 16384 bf16: 1740-1960 us where it does, 810-860 tied; 4-bit
+// 4096 x 4096 x 16384 182 us, 126 tied).  The compiler knows no waits of it: the
+// two states ahead are for an operand that a vector instruction has just written,
+// and sums are read only past settled().
 template <int DT>
-__device__ __forceinline__ f32x4 mfma(const i32x4 a, const i32x4 b, f32x4 c, int sa, int sb, int kk) {
-    if constexpr (DT == DT_BF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else if constexpr (DT == DT_F16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    else {
-        const i32x8 wa = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, wb = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
-        // formats 4: e2m1; byte kk of the scale words
-        if (kk == 0) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, sa, 0, sb);
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 1, sa, 1, sb);
+__device__ __forceinline__ void mfma(f32x4 &c, const i32x4 a, const i32x4 b, int sa, int sb, int byte) {
+    if constexpr (DT == DT_BF16) {
+        asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    } else if constexpr (DT == DT_F16) {
+        asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    } else {
+        // formats 4: e2m1; the operand selects choose byte `byte` of both scale words
+#define GA_MFMA4(SEL) \
+    asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4 blgp:4" \
+        : "+v"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+        if (byte == 0) GA_MFMA4("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+        else if (byte == 1) GA_MFMA4("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+        else if (byte == 2) GA_MFMA4("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+        else GA_MFMA4("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef GA_MFMA4
     }
+}
+
+// Ends the last product: 32 states, the longest of them takes 16 passes' fewer.
+template <int NF, int NT>
+__device__ __forceinline__ void settled(f32x4 (&acc)[NF][NT]) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
 // ---------------------------------------------------------------------------
@@ -252,20 +274,16 @@ template <int DT_, bool AK_, bool BK_, int WF_, int WT_, int NF_, int NT_> struc
     static constexpr int KS = KPerStep<DT>::value;
     static constexpr int LA = FT / 8 / W, LB = TT / 8 / W;  // 1024-byte loads a wavefront and step
     static_assert(LA * 8 * W == FT && LB * 8 * W == TT, "loads");
-    static_assert(DT != DT_MX4 || (!AK && !BK && W * 64 == FT + TT), "one row's scales a thread");
+    static_assert(DT != DT_MX4 || (!AK && !BK), "scales");
 };
 
-// Eight scales of a row at block b; the row's tail reads as 2^-127 (codes past it are zero).
-__device__ __forceinline__ uint2 scales8(const uint8_t *row, int32_t b, int32_t blocks) {
-    if (b + 8 <= blocks) {
-        const u32x2 v = *reinterpret_cast<const u32x2_a1 *>(row + b);
-        return uint2{v.x, v.y};
-    }
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (b + e < blocks) w[e >> 2] |= (uint32_t)row[b + e] << ((e & 3) * 8);
-    return uint2{w[0], w[1]};
+// The feature (of D, or of either half's) that row `row` of a contiguous A tile
+// holds.  Rows 8 W apart are equally many features apart for every lane.
+template <int NF, bool GATED>
+__device__ __forceinline__ constexpr uint32_t feature_of(uint32_t row) {
+    const uint32_t m = row & 15, frag = row / 16 % NF;
+    return GATED ? row / (16 * NF) * (8 * NF) + (m >> 2) * (2 * NF) + frag % (NF / 2) * 4 + (m & 3)
+                 : row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3);
 }
 
 template <typename C, int EPI, int ACT, int OUT>
@@ -279,8 +297,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t b0[TT * STEP_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t b1[TT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint2 sc0[MX ? FT + TT : 1];
-    __shared__ __attribute__((aligned(16))) uint2 sc1[MX ? FT + TT : 1];
+    __shared__ uint4 sc[MX ? 3 * (FT + TT) : 1];  // MX4: a row's scales of two steps, twice, and the last ones
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, wf = wave / C::WT, wt = wave % C::WT;
@@ -300,40 +317,27 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     const int32_t steps = ke > kb ? (ke - kb + C::KS - 1) / C::KS : 0;
 
     // ---- what this lane loads ----
-    uint32_t va[C::LA], vb[C::LB];
-    uint32_t chunk_a[C::LA], chunk_b[C::LB];  // contiguous operands: the chunk of the row's 128 bytes
-#pragma unroll
-    for (int j = 0; j < C::LA; ++j) {
-        const int i = j * W + wave;
-        if constexpr (C::AK) {
-            constexpr int CPR = FT / 8, RPI = 64 / CPR;
-            const uint32_t k = i * RPI + lane / CPR;
-            va[j] = k * (uint32_t)p.a_row + (((lane % CPR) ^ swizzle_a<NF>(k)) * 16);
-        } else {
-            const uint32_t row = i * 8 + (lane >> 3), m = row & 15;
-            chunk_a[j] = (lane & 7) ^ (row >> 1 & 7);
-            uint32_t frag = row / 16 % NF;
-            if constexpr (GATED) {
-                frag %= NF / 2;
-                va[j] = (row / (16 * NF) * (8 * NF) + (m >> 2) * (2 * NF) + frag * 4 + (m & 3)) * (uint32_t)p.a_row;
-            } else {
-                va[j] = (row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3)) * (uint32_t)p.a_row;
-            }
-            va[j] += chunk_a[j] * 16;
-        }
+    // One offset a lane and operand: load j of a wavefront is 8 W rows (or as many
+    // k) further on for every lane, which is a uniform offset.
+    uint32_t va, vb;
+    uint32_t chunk_a, chunk_b;  // contiguous operands: the chunk of the row's 128 bytes
+    if constexpr (C::AK) {
+        constexpr int CPR = FT / 8, RPI = 64 / CPR;
+        const uint32_t k = wave * RPI + lane / CPR;
+        va = k * (uint32_t)p.a_row + ((lane % CPR) ^ swizzle_a<NF>(k)) * 16;
+    } else {
+        const uint32_t row = wave * 8 + (lane >> 3);
+        chunk_a = (lane & 7) ^ (row >> 1 & 7);
+        va = feature_of<NF, GATED>(row) * (uint32_t)p.a_row + chunk_a * 16;
     }
-#pragma unroll
-    for (int j = 0; j < C::LB; ++j) {
-        const int i = j * W + wave;
-        if constexpr (C::BK) {
-            constexpr int CPR = TT / 8, RPI = 64 / CPR;
-            const uint32_t k = i * RPI + lane / CPR;
-            vb[j] = k * (uint32_t)p.b_row + (((lane % CPR) ^ swizzle_b(k)) * 16);
-        } else {
-            const uint32_t row = i * 8 + (lane >> 3);
-            chunk_b[j] = (lane & 7) ^ (row >> 1 & 7);
-            vb[j] = row * (uint32_t)p.b_row + chunk_b[j] * 16;
-        }
+    if constexpr (C::BK) {
+        constexpr int CPR = TT / 8, RPI = 64 / CPR;
+        const uint32_t k = wave * RPI + lane / CPR;
+        vb = k * (uint32_t)p.b_row + ((lane % CPR) ^ swizzle_b(k)) * 16;
+    } else {
+        const uint32_t row = wave * 8 + (lane >> 3);
+        chunk_b = (lane & 7) ^ (row >> 1 & 7);
+        vb = row * (uint32_t)p.b_row + chunk_b * 16;
     }
     const uint8_t *a = (const uint8_t *)p.a, *b = (const uint8_t *)p.b;
     const int32_t rows_a = p.F - f0 < FW ? p.F - f0 : FW, rows_b = T - t0 < TT ? T - t0 : TT;
@@ -344,66 +348,83 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     }
     if constexpr (!C::BK) wb = window(b + t0 * p.b_row, rows_b * p.b_row);
 
-    // MX4: the row whose scales this thread brings
-    const uint8_t *scale_row = nullptr;
+    // MX4: the row whose scales this thread brings, from the tile's first
+    __amdgpu_buffer_rsrc_t ws = wa;
+    uint32_t vs = 0;
+    const int32_t first_block = kb / MX_BLOCK, blocks = MX ? (ke - kb + MX_BLOCK - 1) / MX_BLOCK : 0;  // of this slice
     if constexpr (MX) {
-        if ((int)threadIdx.x < FT) {
-            const uint32_t row = threadIdx.x, m = row & 15;
-            uint32_t frag = row / 16 % NF, f;
-            bool up = false;
-            if constexpr (GATED) {
-                up = frag >= NF / 2;
-                frag %= NF / 2;
-                f = row / (16 * NF) * (8 * NF) + (m >> 2) * (2 * NF) + frag * 4 + (m & 3);
-            } else {
-                f = row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3);
-            }
-            int64_t at = f0 + f < (uint32_t)p.F ? f0 + f : p.F - 1;  // past the end: any row, not stored
-            if (up) at += p.F;
-            scale_row = p.a_scales + at * p.blocks;
+        if (wave < FT / 64) {
+            const uint32_t row = threadIdx.x;
+            vs = feature_of<NF, GATED>(row) * (uint32_t)p.blocks;
+            if (GATED && row / 16 % NF >= NF / 2) vs += (uint32_t)p.F * (uint32_t)p.blocks;
+            ws = window(p.a_scales + (int64_t)f0 * p.blocks, ((GATED ? 2 * (int64_t)p.F : p.F) - f0) * p.blocks);
         } else {
-            const int32_t t = t0 + (int)threadIdx.x - FT;
-            scale_row = p.b_scales + (int64_t)(t < T ? t : T - 1) * p.blocks;
+            vs = (threadIdx.x - FT) * (uint32_t)p.blocks;
+            ws = window(p.b_scales + (int64_t)t0 * p.blocks, (int64_t)rows_b * p.blocks);
         }
+        vs += first_block;
     }
 
-    const auto load = [&](int32_t s, uint8_t *la, uint8_t *lb) {
+    // The loads of step s: where they read (aim), and one of them.
+    uint32_t oa, ob;
+    int so;
+    const auto aim = [&](int32_t s) {
         const int32_t k0 = kb + s * C::KS;
         const bool tail = k0 + C::KS > ke;
-        // values of this step that are there; a row of 4-bit codes ends with its last block's 16 bytes
-        const uint32_t chunks = MX ? (uint32_t)((ke - k0 + 31) / 32) : (uint32_t)((ke - k0 + 7) / 8);
+        // chunks of this step that are there; a row of 4-bit codes ends with its last block's 16 bytes
+        const uint32_t chunks = k0 >= ke ? 0 : MX ? (uint32_t)((ke - k0 + 31) / 32) : (uint32_t)((ke - k0 + 7) / 8);
         if constexpr (C::AK)
             wa = window(a + k0 * p.a_row + (int64_t)f0 * 2, (int64_t)(tail ? ke - k0 : C::KS) * p.a_row - (int64_t)f0 * 2);
         if constexpr (C::BK)
             wb = window(b + k0 * p.b_row + (int64_t)t0 * 2, (int64_t)(tail ? ke - k0 : C::KS) * p.b_row - (int64_t)t0 * 2);
-        const int so = MX ? k0 / 2 : k0 * 2;
-#pragma unroll
-        for (int j = 0; j < C::LA; ++j) {
+        so = MX ? k0 / 2 : k0 * 2;
+        oa = !C::AK && tail && chunk_a >= chunks ? FAR : va, ob = !C::BK && tail && chunk_b >= chunks ? FAR : vb;
+    };
+    const auto load_one = [&](int j, uint8_t *la, uint8_t *lb) {
+        if (j < C::LA) {
             uint8_t *at = la + (j * W + wave) * 1024;
             if constexpr (C::AK) {
-                to_lds(wa, at, va[j], 0);
+                to_lds(wa, at, oa, (int)(j * W * 64 / (FT / 8) * p.a_row));
             } else {
                 const bool up = GATED && (j * W + wave) / 2 % NF >= NF / 2;
-                to_lds(up ? wu : wa, at, tail && chunk_a[j] >= chunks ? FAR : va[j], so);
+                to_lds(up ? wu : wa, at, oa, so + (int)(feature_of<NF, GATED>(j * W * 8) * p.a_row));
             }
-        }
-#pragma unroll
-        for (int j = 0; j < C::LB; ++j) {
+        } else {
+            j -= C::LA;
             uint8_t *at = lb + (j * W + wave) * 1024;
-            if constexpr (C::BK) to_lds(wb, at, vb[j], 0);
-            else to_lds(wb, at, tail && chunk_b[j] >= chunks ? FAR : vb[j], so);
+            if constexpr (C::BK) to_lds(wb, at, ob, (int)(j * W * 64 / (TT / 8) * p.b_row));
+            else to_lds(wb, at, ob, so + (int)(j * W * 8 * p.b_row));
         }
-        // left to itself the compiler moves them down to the wait
-        __builtin_amdgcn_sched_barrier(0);
     };
-    const auto load_scales = [&](int32_t s) -> uint2 {
-        if constexpr (MX) return scales8(scale_row, (kb + s * C::KS) / 32, ke / 32 + (ke % 32 != 0));
-        return uint2{0, 0};
+    const auto load = [&](int32_t s, uint8_t *la, uint8_t *lb) {
+        aim(s);
+#pragma unroll
+        for (int j = 0; j < C::LA + C::LB; ++j) load_one(j, la, lb);
     };
-    // bytes 0 4 1 5 | 2 6 3 7: lane group g reads the pair of its two blocks
-    const auto put_scales = [&](uint2 v, uint2 *to) {
-        if constexpr (MX)
-            to[threadIdx.x] = uint2{__builtin_amdgcn_perm(v.y, v.x, 0x05010400u), __builtin_amdgcn_perm(v.y, v.x, 0x07030602u)};
+
+    // Scales go through registers, 16 of a row for two steps at a time: into one
+    // of two halves of sc, or where the slice ends within the 16, once and byte by
+    // byte at the start, into the third.  (A branch to the byte loads inside the
+    // loop made the compiler wait for every load in flight: 308 us against 187
+    // without any scale, 4096 x 4096 x 16384.)
+    const auto load_scales = [&](int32_t w) -> u32x4 {
+        return __builtin_amdgcn_raw_buffer_load_b128(ws, vs + w * 16, 0, 0);
+    };
+    // Bytes b of words 0 .. 3 become word b: lane group g reads the scales of its
+    // block of both instructions of both steps.
+    const auto put_scales = [&](u32x4 v, uint4 *to) {
+        const uint32_t lo0 = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u), hi0 = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
+        const uint32_t lo1 = __builtin_amdgcn_perm(v.w, v.z, 0x05010400u), hi1 = __builtin_amdgcn_perm(v.w, v.z, 0x07030602u);
+        to[threadIdx.x] = uint4{__builtin_amdgcn_perm(lo1, lo0, 0x05040100u), __builtin_amdgcn_perm(lo1, lo0, 0x07060302u),
+                                __builtin_amdgcn_perm(hi1, hi0, 0x05040100u), __builtin_amdgcn_perm(hi1, hi0, 0x07060302u)};
+    };
+    const auto put_last_scales = [&] {
+        u32x4 v = {0, 0, 0, 0};  // 2^-127: the codes there are zero
+#pragma unroll
+        for (int e = 0; e < 15; ++e)
+            if (e < blocks % 16)
+                v[e / 4] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(ws, vs + blocks / 16 * 16 + e, 0, 0) << (e % 4 * 8);
+        put_scales(v, sc + 2 * (FT + TT));
     };
 
     // ---- fragments ----
@@ -420,89 +441,132 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
         return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)at);
     };
     const int q = r & 3, kr = r >> 2;
-    const auto compute = [&](const uint8_t *la, const uint8_t *lb, const uint2 *sc) {
-        int sa[NF], sb[NT];
-        if constexpr (MX) {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(sc);
-#pragma unroll
-            for (int i = 0; i < NF; ++i) sa[i] = h[(wf * NF * 16 + i * 16 + r) * 4 + g];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) sb[j] = h[(FT + wt * NT * 16 + j * 16 + r) * 4 + g];
-        }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            i32x4 fa[NF], fb[NT];
-#pragma unroll
-            for (int i = 0; i < NF; ++i) {
-                if constexpr (C::AK) {
-                    const uint32_t k = kk * 32 + g * 8 + kr;
-                    const uint32_t chunk = ((wf * NF * 16 + q * NF * 4 + i * 4) / 8) ^ swizzle_a<NF>(kr);
-                    const uint8_t *at = la + k * (FT * 2) + chunk * 16 + (i & 1) * 8;
-                    const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * FT * 2);
-                    fa[i] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                } else {
-                    fa[i] = read_row(la, wf * NF * 16 + i * 16, kk);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if constexpr (C::BK) {
-                    const uint32_t k = kk * 32 + g * 8 + kr;
-                    const uint32_t chunk = ((wt * NT + j) * 2 + (q >> 1)) ^ swizzle_b(kr);
-                    const uint8_t *at = lb + k * (TT * 2) + chunk * 16 + (q & 1) * 8;
-                    const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * TT * 2);
-                    fb[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                } else {
-                    fb[j] = read_row(lb, wt * NT * 16 + j * 16, kk);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j], MX ? sa[i] : 0, MX ? sb[j] : 0, kk);
+    const auto read_b = [&](const uint8_t *lb, int kk, int j) -> i32x4 {
+        if constexpr (C::BK) {
+            const uint32_t k = kk * 32 + g * 8 + kr;
+            const uint32_t chunk = ((wt * NT + j) * 2 + (q >> 1)) ^ swizzle_b(kr);
+            const uint8_t *at = lb + k * (TT * 2) + chunk * 16 + (q & 1) * 8;
+            const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * TT * 2);
+            return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return read_row(lb, (wt * NT + j) * 16, kk);
         }
     };
-
+    const auto read_a = [&](const uint8_t *la, int kk, int i) -> i32x4 {
+        if constexpr (C::AK) {
+            const uint32_t k = kk * 32 + g * 8 + kr;
+            const uint32_t chunk = ((wf * NF * 16 + q * NF * 4 + i * 4) / 8) ^ swizzle_a<NF>(kr);
+            const uint8_t *at = la + k * (FT * 2) + chunk * 16 + (i & 1) * 8;
+            const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * FT * 2);
+            return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return read_row(la, (wf * NF + i) * 16, kk);
+        }
+    };
+    // Half a step: multiplies (fa, fb), by rows of the tile; beside the rows' products
+    // reads the next fragments (na, nb) from half kk of (la, lb) and, where LOAD,
+    // issues the loads aimed into (da, db), a few a row: all at once they hold up
+    // the wavefronts' other work (gated 16384 x 8192 x 4096: 1660 us, 1600 spread).
+    const auto phase = [&](const i32x4 (&fa)[NF], const i32x4 (&fb)[NT], const int (&sa)[NF], const int (&sb)[NT], auto byte,
+                           const uint8_t *la, const uint8_t *lb, int kk, i32x4 (&na)[NF], i32x4 (&nb)[NT], auto load,
+                           uint8_t *da, uint8_t *db) {
+        constexpr int READS = (NF + NT + NF - 3) / (NF - 2), LOADS = (C::LA + C::LB + NF - 1) / NF;  // a row
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+#pragma unroll
+            for (int e = i * READS; e < (i + 1) * READS && e < NF + NT; ++e) {
+                if (e < NT) nb[e] = read_b(lb, kk, e);
+                else na[e - NT] = read_a(la, kk, e - NT);
+            }
+            if constexpr (decltype(load)::value) {
+#pragma unroll
+                for (int j = i * LOADS; j < (i + 1) * LOADS && j < C::LA + C::LB; ++j) load_one(j, da, db);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mfma<DT>(acc[i][j], fa[i], fb[j], sa[i], sb[j], decltype(byte)::value);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const auto read_scales = [&](int32_t w, int (&sa)[NF], int (&sb)[NT]) {
+        const uint32_t *h = reinterpret_cast<const uint32_t *>(sc + (w * 16 + 16 > blocks ? 2 : w & 1) * (FT + TT));
+#pragma unroll
+        for (int i = 0; i < NF; ++i) sa[i] = h[((wf * NF + i) * 16 + r) * 4 + g];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sb[j] = h[(FT + (wt * NT + j) * 16 + r) * 4 + g];
+    };
     const auto landed = [] {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
         __syncthreads();
     };
+    // A step's second fragments are read while its first are multiplied, and the
+    // next step's first while its second are: the barrier between has products
+    // queued on either side.  Past it the step's own half of LDS is free for the
+    // loads of the step after the next.  Loads of steps that are not there read
+    // nothing (their offsets are past the end).
+    i32x4 fa0[NF], fa1[NF], fb0[NT], fb1[NT];
+    int sa[NF], sb[NT];
+    const std::integral_constant<int, 0> first;
+    const std::integral_constant<int, 1> second;
+    const std::integral_constant<int, 2> third;
+    const std::integral_constant<int, 3> fourth;
+    const std::true_type loads;
+    const std::false_type none;
     if (steps > 0) {
         load(0, a0, b0);
-        put_scales(load_scales(0), sc0);
-        landed();
-    }
-    uint2 next{};
-    for (int32_t s = 0; s + 2 <= steps; s += 2) {
-        load(s + 1, a1, b1);
-        next = load_scales(s + 1);
-        compute(a0, b0, sc0);
-        put_scales(next, sc1);
-        landed();
-        if (s + 2 < steps) {
-            load(s + 2, a0, b0);
-            next = load_scales(s + 2);
+        if constexpr (MX) {
+            put_scales(load_scales(0), sc);
+            if (blocks % 16 != 0) put_last_scales();
         }
-        compute(a1, b1, sc1);
-        put_scales(next, sc0);
         landed();
+        load(1, a1, b1);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb0[j] = read_b(b0, 0, j);
+#pragma unroll
+        for (int i = 0; i < NF; ++i) fa0[i] = read_a(a0, 0, i);
+        if constexpr (MX) read_scales(0, sa, sb);
     }
-    if (steps & 1) compute(a0, b0, sc0);
+    for (int32_t s = 0; s + 2 <= steps; s += 2) {
+        u32x4 next{};
+        int na[NF], nb[NT];
+        if constexpr (MX) next = load_scales(s / 2 + 1);
+        phase(fa0, fb0, sa, sb, first, a0, b0, 1, fa1, fb1, none, a0, b0);
+        aim(s + 2);
+        landed();
+        phase(fa1, fb1, sa, sb, second, a1, b1, 0, fa0, fb0, loads, a0, b0);
+        phase(fa0, fb0, sa, sb, third, a1, b1, 1, fa1, fb1, none, a1, b1);
+        if constexpr (MX) put_scales(next, sc + ((s / 2 + 1) & 1) * (FT + TT));
+        aim(s + 3);
+        landed();
+        if constexpr (MX) read_scales(s / 2 + 1, na, nb);
+        phase(fa1, fb1, sa, sb, fourth, a0, b0, 0, fa0, fb0, loads, a1, b1);
+        if constexpr (MX) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i) sa[i] = na[i];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sb[j] = nb[j];
+        }
+    }
+    if (steps & 1) {
+        phase(fa0, fb0, sa, sb, first, a0, b0, 1, fa1, fb1, none, a0, b0);
+        phase(fa1, fb1, sa, sb, second, a0, b0, 1, fa0, fb0, none, a0, b0);
+    }
+    settled(acc);
 
     // ---- epilogue ----
-    // Through LDS, 16 KB a wavefront and JT x 16 tokens at a time, so that a lane
+    // Through LDS, SPACE bytes a wavefront and JT x 16 tokens at a time, so that a lane
     // ends up with eight consecutive features and neighbouring lanes with the
     // next ones.  (Straight from the accumulators the unrolled epilogue spills.)
     // Four results of a lane are 16 bytes of a token's row; chunk c of token t
     // sits in c ^ t % 16, so that 16 tokens' writes fall into all banks.
-    constexpr int JT = 16 * 1024 / (NF * 16 * 16 * 4), CHUNKS = NF * 4;  // chunks a token
-    static_assert(NT % JT == 0 && FT * STEP_BYTES >= 16 * 1024 && W * 16 * 1024 == 2 * (FT + TT) * STEP_BYTES, "16 KB a wavefront");
-    constexpr int PER = FT * STEP_BYTES / (16 * 1024);  // wavefronts an array
-    uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == 1 ? b0 : wave / PER == 2 ? a1 : b1) + wave % PER * (16 * 1024);
+    constexpr int SPACE = 2 * (FT + TT) * STEP_BYTES / W;  // a wavefront's
+    constexpr int JT = SPACE / (NF * 16 * 16 * 4), CHUNKS = NF * 4;  // chunks a token
+    static_assert(NT % JT == 0 && FT == TT && W % 4 == 0, "the four arrays, shared alike");
+    constexpr int PER = W / 4;  // wavefronts an array
+    uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == 1 ? b0 : wave / PER == 2 ? a1 : b1) + wave % PER * SPACE;
     constexpr int LANES = CHUNKS / (GATED ? 4 : 2), TOKENS = 64 / LANES;  // lanes a token, tokens a pass
     const int oct = lane % LANES;
     const int32_t f = f0 + wf * (LANES * 8) + oct * 8;
-    __syncthreads();
+    landed();
 #pragma unroll
     for (int half = 0; half < NT / JT; ++half) {
 #pragma unroll
