@@ -14,7 +14,7 @@
 //
 // h and dz are rounded to the type, as the matrix cores take them; dh, the
 // activation and its slope stay in fp32.
-#include "ga_tile.h"
+#include "ga_stream.h"
 
 namespace ga {
 
@@ -28,7 +28,7 @@ template <int DT, bool A, bool B> using Mid = Tile<DT, A, B, 2, 2, 4, 4>;
 
 template <int DT, bool A, bool B, int EPI, int ACT>
 hipError_t product(const TileArgs &p, bool halves, float *partial, hipStream_t stream) {
-    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, KPerStep<DT>::value);
+    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, !A && !B, KPerStep<DT>::value);
     return launch_product<Big<DT, A, B>, Mid<DT, A, B>, EPI, ACT, DT>(p, plan, halves, partial, stream);
 }
 
@@ -121,7 +121,7 @@ hipError_t backward_op(int op, const void *dy, const void *x, const void *kept, 
 
 // Tiles of 256 x 256 where they fill the card, else of 128 x 128 with k in
 // slices until two workgroups a compute unit are there or a slice is short.
-ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int step) {
+ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step) {
     constexpr int64_t CUS = 256, LEAST_STEPS = 8;
     const auto tiles = [&](int64_t side) {
         const int64_t fw = halves ? side / 2 : side;
@@ -130,7 +130,10 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int step)
     ProductPlan p{PRODUCT_BIG, 1, 0, tiles(256), 0};
     const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
     int64_t splits = 1;
-    if (p.workgroups < CUS * 3 / 4) {
+    if (contiguous && T <= PRODUCT_FEW_TOKENS) {
+        p.tile = PRODUCT_FEW;
+        p.workgroups = (F + 7) / 8;  // at most
+    } else if (p.workgroups < CUS * 3 / 4) {
         p.tile = PRODUCT_MID;
         p.workgroups = tiles(128);
         splits = 2 * CUS / (p.workgroups > 0 ? p.workgroups : 1);
@@ -148,7 +151,7 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int step)
 FeedForwardSpace feed_forward_space(int64_t rows, int64_t H, int64_t d, int halves) {
     FeedForwardSpace s{};
     s.partial = align256((size_t)rows * d * 2);
-    const size_t a = plan_product(d, rows, H, halves == 2, 64).partial_bytes, b = plan_product(H, rows, d, false, 64).partial_bytes;
+    const size_t a = plan_product(d, rows, H, halves == 2, true, 64).partial_bytes, b = plan_product(H, rows, d, false, true, 64).partial_bytes;
     s.total = s.partial + align256(a > b ? a : b);
     return s;
 }
@@ -157,10 +160,10 @@ FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d,
     FeedForwardSpace s{};
     s.gradient = align256((size_t)rows * d * 2);
     s.partial = s.gradient + align256((size_t)rows * halves * d * 2);
-    const size_t parts[4] = {plan_product(d, rows, H, false, 64).partial_bytes,
-                             plan_product(H, rows, halves * d, false, 64).partial_bytes,
-                             plan_product(H, halves * d, rows, false, 64).partial_bytes,
-                             plan_product(d, H, rows, false, 64).partial_bytes};
+    const size_t parts[4] = {plan_product(d, rows, H, false, false, 64).partial_bytes,
+                             plan_product(H, rows, halves * d, false, false, 64).partial_bytes,
+                             plan_product(H, halves * d, rows, false, false, 64).partial_bytes,
+                             plan_product(d, H, rows, false, false, 64).partial_bytes};
     size_t most = 0;
     for (size_t b : parts) most = b > most ? b : most;
     s.total = s.partial + align256(most);

@@ -194,19 +194,23 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
 // The feed-forward layer's products, 16-bit and microscaled 4-bit operands
 // (ga_tile.h, ga_mx.h).
 // ---------------------------------------------------------------------------
-// Tile and slices of one product of F features, T tokens and K values: tiles of
-// 256 or 128 features (half as many where a gate and an up half share a tile)
-// and tokens, k in `splits` slices of k_split values whose partial sums a second
-// launch adds (splits * T * F fp32, twice that with two halves).
-enum : int { PRODUCT_BIG, PRODUCT_MID };
+// How one product of F features, T tokens and K values runs: up to
+// PRODUCT_FEW_TOKENS tokens, both operands with k contiguous, as a stream of the
+// weights (ga_stream.h); else in tiles of 256 or 128 features (half as many where
+// a gate and an up half share a tile) and tokens (ga_tile.h), k in `splits` slices
+// of k_split values whose partial sums a second launch adds (splits * T * F fp32,
+// twice that with two halves).
+enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_FEW };
+constexpr int64_t PRODUCT_FEW_TOKENS = 16;
 struct ProductPlan {
     int tile, splits;
     int32_t k_split;
     int64_t workgroups;
     size_t partial_bytes;
 };
-// step: values of k a step (64 of 16 bits, 256 of 4)
-ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int step);
+// contiguous: k is in both operands; step: values of k a step (64 of 16 bits, 256
+// of 4)
+ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step);
 
 // Bytes of workspace, and where its parts begin.
 struct FeedForwardSpace {

@@ -656,21 +656,4 @@ hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t strea
     return launch_kernel(finish_kernel<EPI, ACT, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
 }
 
-// One product with the planner's tile and slices (plan_product, ga_internal.h).
-template <typename Big, typename Mid, int EPI, int ACT, int OUT>
-hipError_t launch_product(TileArgs p, const ProductPlan &plan, bool halves, float *partial, hipStream_t stream) {
-    p.splits = plan.splits;
-    p.k_split = plan.k_split;
-    p.partial = partial;
-    const bool big = plan.tile == PRODUCT_BIG;
-    if (plan.splits == 1)
-        return big ? launch_tile<Big, EPI, ACT, OUT>(p, halves, stream) : launch_tile<Mid, EPI, ACT, OUT>(p, halves, stream);
-    // the slices' sums: with two halves only for the epilogues that join them
-    constexpr bool JOINS = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
-    constexpr int PART_ACT = JOINS ? OP_SILU_MUL : OP_SQUARED_RELU;
-    const hipError_t e = big ? launch_tile<Big, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream)
-                             : launch_tile<Mid, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream);
-    return e != hipSuccess ? e : launch_finish<EPI, ACT, OUT>(p, !Big::BK, stream);
-}
-
 }  // namespace ga

@@ -6,7 +6,7 @@
 //   layer: x is quantised, z = q(x) w_in^T = gate | up stays in fp32, the first
 //          product's epilogue activates and quantises h = act(gate) up, and
 //          y = q(h) w_down^T
-#include "ga_tile.h"
+#include "ga_stream.h"
 
 namespace ga {
 
@@ -27,7 +27,7 @@ hipError_t product(const void *a, const uint8_t *a_scales, const void *w, const 
     p.a = w, p.a_scales = w_scales, p.b = a, p.b_scales = a_scales;
     p.blocks = (int32_t)blocks_of(k), p.a_row = p.b_row = 16 * (int64_t)p.blocks;
     p.F = n, p.T = rows, p.K = p.blocks * MX_BLOCK, p.live = live, p.out = out, p.out2 = out2;
-    return launch_product<Big, Mid, EPI, ACT, OUT>(p, plan_product(n, rows, k, halves, STEP), halves, partial, stream);
+    return launch_product<Big, Mid, EPI, ACT, OUT>(p, plan_product(n, rows, k, halves, true, STEP), halves, partial, stream);
 }
 
 template <int OUT>
@@ -73,7 +73,7 @@ hipError_t layer_op(int op, const void *x, const void *w_in, const uint8_t *w_in
 }  // namespace
 
 size_t mxfp4_product_space(int64_t rows, int64_t n, int64_t k) {
-    return align256(plan_product(n, rows, k, false, STEP).partial_bytes);
+    return align256(plan_product(n, rows, k, false, true, STEP).partial_bytes);
 }
 
 hipError_t launch_mxfp4_product(int dtype, const void *a, const uint8_t *a_scales, const void *w, const uint8_t *w_scales,
@@ -93,7 +93,7 @@ FeedForward4Space feed_forward_mxfp4_space(int64_t rows, int64_t H, int64_t d, i
     s.h_codes = s.x_scales + align256((size_t)rows * blocks_of(H));
     s.h_scales = s.h_codes + align256((size_t)rows * blocks_of(d) * 16);
     s.partial = s.h_scales + align256((size_t)rows * blocks_of(d));
-    const size_t a = plan_product(d, rows, H, halves == 2, STEP).partial_bytes, b = plan_product(H, rows, d, false, STEP).partial_bytes;
+    const size_t a = plan_product(d, rows, H, halves == 2, true, STEP).partial_bytes, b = plan_product(H, rows, d, false, true, STEP).partial_bytes;
     s.total = s.partial + align256(a > b ? a : b);
     return s;
 }
