@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libga.so")
 SOURCES = ["api.hip", "gelu_sparse.hip", "gelu_sparse_split.hip", "gelu_sparse_unaligned.hip", "gelu_sparse_rows.hip",
            "gelu_sparse_rep.hip", "gelu_sparse_decode.hip", "gelu_sparse_staged.hip", "gelu_sparse_tiled.hip",
            "elementwise.hip", "checkpoint.hip", "gelu_sparse_train.hip", "layer_norm.hip", "balance.hip", "train_api.hip",
-           "feed_forward.hip", "mxfp4.hip", "mxfp4_product.hip", "feed_forward_api.hip"]
+           "feed_forward.hip", "feed_forward_f16.hip", "feed_forward_bf16.hip", "feed_forward_backward_f16.hip",
+           "feed_forward_backward_bf16.hip", "mxfp4.hip", "mxfp4_product.hip", "feed_forward_api.hip"]
 ARCH = "gfx950"
 
 

@@ -1,20 +1,7 @@
-// The gated feed-forward layer in 16 bits, gfx950: forward and backward.
-//
-//   z = x w_in^T = gate | up        w_in [2d, H] (gate rows, up rows; squared ReLU [d, H])
-//   h = act(gate) up                rounded to the type
-//   y = h w_down^T                  w_down [H, d]
-//
-// Forward, two products: the first forms gate and up of the same features in one
-// tile and activates them in its epilogue, so z goes to memory only where it is
-// kept; the second is plain.  Backward, from dy, x and the kept z, four:
-//
-//   dh = dy w_down, whose epilogue reads z and leaves dz and h (dh itself is
-//        never stored)
-//   dx = dz w_in,  dw_in = dz^T x,  dw_down = dy^T h
-//
-// h and dz are rounded to the type, as the matrix cores take them; dh, the
-// activation and its slope stay in fp32.
-#include "ga_stream.h"
+// The feed-forward layer on the host: how a product runs, workspaces, and the
+// choice of the element type's kernels.
+#include "ga_device.h"
+#include "ga_internal.h"
 
 namespace ga {
 
@@ -22,123 +9,52 @@ namespace {
 
 constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-constexpr bool KC = false, KS = true;  // k contiguous, strided
-template <int DT, bool A, bool B> using Big = Tile<DT, A, B, 2, 4, 8, 4>;
-template <int DT, bool A, bool B> using Mid = Tile<DT, A, B, 2, 2, 4, 4>;
-
-template <int DT, bool A, bool B, int EPI, int ACT>
-hipError_t product(const TileArgs &p, bool halves, float *partial, hipStream_t stream) {
-    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, !A && !B, KPerStep<DT>::value);
-    return launch_product<Big<DT, A, B>, Mid<DT, A, B>, EPI, ACT, DT>(p, plan, halves, partial, stream);
-}
-
-template <int DT, int ACT>
-hipError_t forward_as(const void *x, const void *w_in, const void *w_down, void *y, void *kept, int32_t rows, int32_t H,
-                      int32_t d, const int32_t *live, uint8_t *workspace, hipStream_t stream) {
-    constexpr bool GATED = act_gated<ACT>();
-    const FeedForwardSpace at = feed_forward_space(rows, H, d, GATED ? 2 : 1);
-    void *h = workspace + at.hidden;
-    float *partial = (float *)(workspace + at.partial);
-    TileArgs p{};
-    p.a = w_in, p.a_row = 2 * (int64_t)H, p.b = x, p.b_row = 2 * (int64_t)H;
-    p.F = d, p.T = rows, p.K = H, p.live = live, p.out = h, p.out2 = kept;
-    hipError_t e = product<DT, KC, KC, EPI_GATED, ACT>(p, GATED, partial, stream);
-    if (e != hipSuccess) return e;
-    p = TileArgs{};
-    p.a = w_down, p.a_row = 2 * (int64_t)d, p.b = h, p.b_row = 2 * (int64_t)d;
-    p.F = H, p.T = rows, p.K = d, p.live = live, p.out = y;
-    return product<DT, KC, KC, EPI_STORE, OP_SQUARED_RELU>(p, false, partial, stream);
-}
-
-template <int DT, int ACT>
-hipError_t backward_as(const void *dy, const void *x, const void *kept, const void *w_in, const void *w_down, void *dx,
-                       void *dw_in, void *dw_down, int32_t rows, int32_t H, int32_t d, const int32_t *live,
-                       uint8_t *workspace, hipStream_t stream) {
-    const int32_t zd = act_gated<ACT>() ? 2 * d : d;
-    const FeedForwardSpace at = feed_forward_backward_space(rows, H, d, zd / d);
-    void *h = workspace + at.hidden, *dz = workspace + at.gradient;
-    float *partial = (float *)(workspace + at.partial);
-    hipError_t e = hipSuccess;
-    TileArgs p{};
-    if (rows > 0) {
-        p.a = w_down, p.a_row = 2 * (int64_t)d, p.b = dy, p.b_row = 2 * (int64_t)H;
-        p.F = d, p.T = rows, p.K = H, p.live = live, p.out = dz, p.out2 = h, p.z = kept;
-        e = product<DT, KS, KC, EPI_BACKWARD, ACT>(p, false, partial, stream);
-        if (e != hipSuccess) return e;
-        p = TileArgs{};
-        p.a = w_in, p.a_row = 2 * (int64_t)H, p.b = dz, p.b_row = 2 * (int64_t)zd;
-        p.F = H, p.T = rows, p.K = zd, p.live = live, p.out = dx;
-        e = product<DT, KS, KC, EPI_STORE, OP_SQUARED_RELU>(p, false, partial, stream);
-        if (e != hipSuccess) return e;
-    }
-    p = TileArgs{};
-    p.a = x, p.a_row = 2 * (int64_t)H, p.b = dz, p.b_row = 2 * (int64_t)zd;
-    p.F = H, p.T = zd, p.K = rows, p.live = live, p.out = dw_in;
-    e = product<DT, KS, KS, EPI_STORE, OP_SQUARED_RELU>(p, false, partial, stream);
-    if (e != hipSuccess) return e;
-    p = TileArgs{};
-    p.a = h, p.a_row = 2 * (int64_t)d, p.b = dy, p.b_row = 2 * (int64_t)H;
-    p.F = d, p.T = H, p.K = rows, p.live = live, p.out = dw_down;
-    return product<DT, KS, KS, EPI_STORE, OP_SQUARED_RELU>(p, false, partial, stream);
-}
-
-template <int DT>
-hipError_t forward_op(int op, const void *x, const void *w_in, const void *w_down, void *y, void *kept, int32_t rows,
-                      int32_t H, int32_t d, const int32_t *live, uint8_t *workspace, hipStream_t stream) {
-    switch (op) {
-    case OP_SILU_MUL: return forward_as<DT, OP_SILU_MUL>(x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
-    case OP_GELU_TANH_MUL:
-        return forward_as<DT, OP_GELU_TANH_MUL>(x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
-    case OP_GELU_ERF_MUL:
-        return forward_as<DT, OP_GELU_ERF_MUL>(x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
-    case OP_SQUARED_RELU:
-        return forward_as<DT, OP_SQUARED_RELU>(x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
-    default: return hipErrorInvalidValue;
-    }
-}
-
-template <int DT>
-hipError_t backward_op(int op, const void *dy, const void *x, const void *kept, const void *w_in, const void *w_down,
-                       void *dx, void *dw_in, void *dw_down, int32_t rows, int32_t H, int32_t d, const int32_t *live,
-                       uint8_t *workspace, hipStream_t stream) {
-    switch (op) {
-    case OP_SILU_MUL:
-        return backward_as<DT, OP_SILU_MUL>(dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace, stream);
-    case OP_GELU_TANH_MUL:
-        return backward_as<DT, OP_GELU_TANH_MUL>(dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace,
-                                                 stream);
-    case OP_GELU_ERF_MUL:
-        return backward_as<DT, OP_GELU_ERF_MUL>(dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace,
-                                                stream);
-    case OP_SQUARED_RELU:
-        return backward_as<DT, OP_SQUARED_RELU>(dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace,
-                                                stream);
-    default: return hipErrorInvalidValue;
-    }
-}
-
 }  // namespace
 
-// Tiles of 256 x 256 where they fill the card, else of 128 x 128 with k in
-// slices until two workgroups a compute unit are there or a slice is short.
+// Which tiles, by how many workgroups they make for the 256 compute units.
+//   256 x 256, one workgroup a unit, where their last round is at least 0.76 full:
+//     128 x 128, two a unit, run at 0.75 to 0.78 of their rate (bf16 8192 x 4096 x
+//     16384 1284 and 974 TFLOP/s; 4-bit 4096 x 4096 x 16384 4370 and 3410), and at
+//     288 and 384 large tiles (bf16 12288 x 2 * 768 x 2048 and 12288 x 2048 x 768)
+//     take 86 us against 96 and 43 against 45.
+//   128 x 128 with two stages, two a unit, where there are more than 256 of them
+//     (bf16 4112 x 1032 x 1001 20.4 us; four stages, one a unit, 26.9).
+//   128 x 64 or else 128 x 128 with four stages, one a unit, where 256 or fewer are
+//     there and the loads' latency counts (bf16 1001 x 1032 x 4112 27.2 us, 128 x
+//     128 37.4, with two stages 49.4; 1032 x 2056 x 1001 128 x 128 13.9, 128 x 64,
+//     289 of them, 19.8).
+// k is cut where most of the card would idle: into slices of at least eight steps
+// until half of it is busy (bf16 64 x 4096 x 8192, 32 tiles: whole 32.8 us, four
+// slices 16.7, eight 18.5), and in two where one workgroup has 192 steps or more.
 ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step) {
-    constexpr int64_t CUS = 256, LEAST_STEPS = 8;
-    const auto tiles = [&](int64_t side) {
-        const int64_t fw = halves ? side / 2 : side;
-        return ((F + fw - 1) / fw) * ((T + side - 1) / side);
-    };
-    ProductPlan p{PRODUCT_BIG, 1, 0, tiles(256), 0};
+    constexpr int64_t CUS = 256, LEAST_STEPS = 8, LONG = 192, MOST_SLICES = 64;
     const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
+    const auto tiles = [&](int64_t features, int64_t tokens) {
+        const int64_t fw = halves ? features / 2 : features;
+        return ((F + fw - 1) / fw) * ((T + tokens - 1) / tokens);
+    };
+    const int64_t big = tiles(256, 256), mid = tiles(128, 128), slim = tiles(128, 64);
     int64_t splits = 1;
+    ProductPlan p{};
     if (contiguous && T <= PRODUCT_FEW_TOKENS) {
         p.tile = PRODUCT_FEW;
         p.workgroups = (F + 7) / 8;  // at most
-    } else if (p.workgroups < CUS * 3 / 4) {
+    } else if (100 * big >= 76 * CUS * ((big + CUS - 1) / CUS)) {
+        p.tile = PRODUCT_BIG;
+        p.workgroups = big;
+    } else if (mid > CUS) {
         p.tile = PRODUCT_MID;
-        p.workgroups = tiles(128);
-        splits = 2 * CUS / (p.workgroups > 0 ? p.workgroups : 1);
+        p.workgroups = mid;
+    } else if (slim > CUS) {
+        p.tile = PRODUCT_DEEP;
+        p.workgroups = mid;
+    } else {
+        p.tile = PRODUCT_SLIM;
+        p.workgroups = slim;
+        splits = slim > 0 ? CUS / 2 / slim : 1;
         splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
-        splits = splits < 1 ? 1 : splits > 64 ? 64 : splits;
+        if (splits < 2 && 2 * slim <= CUS && steps >= LONG) splits = 2;
+        splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
     }
     const int64_t per = (steps + splits - 1) / splits;
     p.splits = (int)((steps + per - 1) / per);
@@ -174,8 +90,8 @@ hipError_t launch_feed_forward(int dtype, int op, const void *x, const void *w_i
                                int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
                                hipStream_t stream) {
     switch (dtype) {
-    case DT_F16: return forward_op<DT_F16>(op, x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
-    case DT_BF16: return forward_op<DT_BF16>(op, x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
+    case DT_F16: return launch_feed_forward_f16(op, x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
+    case DT_BF16: return launch_feed_forward_bf16(op, x, w_in, w_down, y, kept, rows, H, d, live, workspace, stream);
     default: return hipErrorInvalidValue;
     }
 }
@@ -186,9 +102,9 @@ hipError_t launch_feed_forward_backward(int dtype, int op, const void *dy, const
                                         hipStream_t stream) {
     switch (dtype) {
     case DT_F16:
-        return backward_op<DT_F16>(op, dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace, stream);
+        return launch_feed_forward_backward_f16(op, dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace, stream);
     case DT_BF16:
-        return backward_op<DT_BF16>(op, dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace, stream);
+        return launch_feed_forward_backward_bf16(op, dy, x, kept, w_in, w_down, dx, dw_in, dw_down, rows, H, d, live, workspace, stream);
     default: return hipErrorInvalidValue;
     }
 }

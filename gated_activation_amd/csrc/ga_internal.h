@@ -196,11 +196,12 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
 // ---------------------------------------------------------------------------
 // How one product of F features, T tokens and K values runs: up to
 // PRODUCT_FEW_TOKENS tokens, both operands with k contiguous, as a stream of the
-// weights (ga_stream.h); else in tiles of 256 or 128 features (half as many where
-// a gate and an up half share a tile) and tokens (ga_tile.h), k in `splits` slices
-// of k_split values whose partial sums a second launch adds (splits * T * F fp32,
-// twice that with two halves).
-enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_FEW };
+// weights (ga_stream.h); else in tiles (ga_tile.h) of 256 features (half as many
+// where a gate and an up half share a tile) x 256 tokens, 128 x 128 with two or
+// four stages (DEEP), or 128 x 64, these with k in `splits` slices of k_split values
+// whose partial sums a second launch adds (splits * T * F fp32, twice that with two
+// halves).
+enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_FEW };
 constexpr int64_t PRODUCT_FEW_TOKENS = 16;
 struct ProductPlan {
     int tile, splits;
@@ -219,7 +220,21 @@ struct FeedForwardSpace {
 FeedForwardSpace feed_forward_space(int64_t rows, int64_t H, int64_t d, int halves);
 FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d, int halves);
 
-// op: OP_* above; kept may be null.
+// op: OP_* above; kept may be null.  _f16, _bf16: of one type.
+hipError_t launch_feed_forward_f16(int op, const void *x, const void *w_in, const void *w_down, void *y, void *kept,
+                                   int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                                   hipStream_t stream);
+hipError_t launch_feed_forward_bf16(int op, const void *x, const void *w_in, const void *w_down, void *y, void *kept,
+                                    int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                                    hipStream_t stream);
+hipError_t launch_feed_forward_backward_f16(int op, const void *dy, const void *x, const void *kept, const void *w_in,
+                                            const void *w_down, void *dx, void *dw_in, void *dw_down, int32_t rows,
+                                            int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                                            hipStream_t stream);
+hipError_t launch_feed_forward_backward_bf16(int op, const void *dy, const void *x, const void *kept, const void *w_in,
+                                             const void *w_down, void *dx, void *dw_in, void *dw_down, int32_t rows,
+                                             int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
+                                             hipStream_t stream);
 hipError_t launch_feed_forward(int dtype, int op, const void *x, const void *w_in, const void *w_down, void *y, void *kept,
                                int32_t rows, int32_t H, int32_t d, const int32_t *live, uint8_t *workspace,
                                hipStream_t stream);

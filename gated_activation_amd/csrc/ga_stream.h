@@ -50,10 +50,10 @@ __device__ __forceinline__ f32x4 mfma_of(const i32x4 a, const i32x4 b, f32x4 c, 
     }
 }
 
-template <int DT, int NF, int NT, int FG, int EPI, int ACT, int OUT>
+template <int DT, int NF, int NT, int FG, int EPI, bool PAIR, int OUT>
 __global__ __launch_bounds__(STREAM_WAVES * 64) void stream_kernel(TileArgs p) {
     constexpr bool MX = DT == DT_MX4;
-    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
     constexpr int WK = STREAM_WAVES / FG;          // wavefronts that share k
     constexpr int HALF = GATED ? NF / 2 : NF;      // fragments of a half
     constexpr int FW = HALF * 4 * FG;              // features of D a workgroup
@@ -148,15 +148,15 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void stream_kernel(TileArgs p) {
         get(0, v);
         if constexpr (GATED) get(1, u);
         const int32_t f = f0 + oct * 8;
-        finish8<EPI, ACT, OUT>(p, t, f, t < T && f < p.F, v, u);
+        finish8<EPI, PAIR, OUT>(p, t, f, t < T && f < p.F, v, u);
     }
 }
 
-template <int DT, int NF, int NT, int FG, int EPI, int ACT, int OUT>
+template <int DT, int NF, int NT, int FG, int EPI, bool PAIR, int OUT>
 hipError_t launch_stream(const TileArgs &p, hipStream_t stream) {
-    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
     constexpr int64_t FW = (GATED ? NF / 2 : NF) * 4 * FG;
-    return launch_kernel(stream_kernel<DT, NF, NT, FG, EPI, ACT, OUT>, dim3((uint32_t)((p.F + FW - 1) / FW)),
+    return launch_kernel(stream_kernel<DT, NF, NT, FG, EPI, PAIR, OUT>, dim3((uint32_t)((p.F + FW - 1) / FW)),
                          dim3(STREAM_WAVES * 64), stream, p);
 }
 
@@ -165,43 +165,50 @@ hipError_t launch_stream(const TileArgs &p, hipStream_t stream) {
 // 11.8, 2048 features 6.7 against 7.0.  Gated in 16 bits: eight, or 32 from nine
 // tokens on, whose loads they share: 16384 features of 2048, one token 26.4 us
 // against 29.2, sixteen 33.5 against 30.8.
-template <int DT, int EPI, int ACT, int OUT, int NT>
+template <int DT, int EPI, bool PAIR, int OUT, int NT>
 hipError_t launch_stream_tokens(const TileArgs &p, hipStream_t stream) {
     if constexpr (EPI == EPI_QUANTIZE) {
-        return launch_stream<DT, act_gated<ACT>() ? 4 : 2, NT, 4, EPI, ACT, OUT>(p, stream);
-    } else if constexpr (EPI == EPI_GATED && act_gated<ACT>()) {
-        return launch_stream<DT, 4, NT, NT == 4 ? 4 : 1, EPI, ACT, OUT>(p, stream);
+        return launch_stream<DT, PAIR ? 4 : 2, NT, 4, EPI, PAIR, OUT>(p, stream);
+    } else if constexpr (EPI == EPI_GATED && PAIR) {
+        return launch_stream<DT, 4, NT, NT == 4 ? 4 : 1, EPI, PAIR, OUT>(p, stream);
     } else {
-        return p.F >= 4096 ? launch_stream<DT, 4, NT, 1, EPI, ACT, OUT>(p, stream)
-                           : launch_stream<DT, 2, NT, 1, EPI, ACT, OUT>(p, stream);
+        return p.F >= 4096 ? launch_stream<DT, 4, NT, 1, EPI, PAIR, OUT>(p, stream)
+                           : launch_stream<DT, 2, NT, 1, EPI, PAIR, OUT>(p, stream);
     }
 }
 
-template <int DT, int EPI, int ACT, int OUT>
+template <int DT, int EPI, bool PAIR, int OUT>
 hipError_t launch_few(const TileArgs &p, hipStream_t stream) {
-    return p.T <= 4   ? launch_stream_tokens<DT, EPI, ACT, OUT, 1>(p, stream)
-           : p.T <= 8 ? launch_stream_tokens<DT, EPI, ACT, OUT, 2>(p, stream)
-                      : launch_stream_tokens<DT, EPI, ACT, OUT, 4>(p, stream);
+    return p.T <= 4   ? launch_stream_tokens<DT, EPI, PAIR, OUT, 1>(p, stream)
+           : p.T <= 8 ? launch_stream_tokens<DT, EPI, PAIR, OUT, 2>(p, stream)
+                      : launch_stream_tokens<DT, EPI, PAIR, OUT, 4>(p, stream);
 }
 
 // One product with the planner's choice (plan_product, ga_internal.h).
-template <typename Big, typename Mid, int EPI, int ACT, int OUT>
-hipError_t launch_product(TileArgs p, const ProductPlan &plan, bool halves, float *partial, hipStream_t stream) {
+template <int DT, bool AK, bool BK, int EPI, bool PAIR, int OUT>
+hipError_t launch_product(TileArgs p, bool halves, float *partial, hipStream_t stream) {
+    using Big = Tile<DT, AK, BK, 2, 4, 8, 4>;
+    using Mid = Tile<DT, AK, BK, 2, 2, 4, 4>;
+    using Deep = Tile<DT, AK, BK, 2, 2, 4, 4, 4>;
+    using Slim = Tile<DT, AK, BK, 2, 2, 4, 2, 4>;
+    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, !AK && !BK, KPerStep<DT>::value);
     p.splits = plan.splits;
     p.k_split = plan.k_split;
     p.partial = partial;
-    if constexpr (!Big::AK && !Big::BK) {
-        if (plan.tile == PRODUCT_FEW) return launch_few<Big::DT, EPI, ACT, EPI == EPI_QUANTIZE ? DT_F32 : OUT>(p, stream);
+    switch (plan.tile) {
+    case PRODUCT_BIG: return launch_tile<Big, EPI, PAIR, OUT>(p, halves, stream);
+    case PRODUCT_MID: return launch_tile<Mid, EPI, PAIR, OUT>(p, halves, stream);
+    case PRODUCT_DEEP: return launch_tile<Deep, EPI, PAIR, OUT>(p, halves, stream);
+    case PRODUCT_SLIM: break;
+    default:
+        if constexpr (!AK && !BK) return launch_few<DT, EPI, PAIR, OUT>(p, stream);
+        return hipErrorInvalidValue;
     }
-    const bool big = plan.tile == PRODUCT_BIG;
-    if (plan.splits == 1)
-        return big ? launch_tile<Big, EPI, ACT, OUT>(p, halves, stream) : launch_tile<Mid, EPI, ACT, OUT>(p, halves, stream);
+    if (plan.splits == 1) return launch_tile<Slim, EPI, PAIR, OUT>(p, halves, stream);
     // the slices' sums: with two halves only for the epilogues that join them
-    constexpr bool JOINS = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
-    constexpr int PART_ACT = JOINS ? OP_SILU_MUL : OP_SQUARED_RELU;
-    const hipError_t e = big ? launch_tile<Big, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream)
-                             : launch_tile<Mid, EPI_PARTIAL, PART_ACT, DT_F32>(p, halves, stream);
-    return e != hipSuccess ? e : launch_finish<EPI, ACT, OUT>(p, !Big::BK, stream);
+    constexpr bool JOINS = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
+    const hipError_t e = launch_tile<Slim, EPI_PARTIAL, JOINS, DT_F32>(p, halves, stream);
+    return e != hipSuccess ? e : launch_finish<EPI, PAIR, OUT>(p, !BK, stream);
 }
 
 }  // namespace ga

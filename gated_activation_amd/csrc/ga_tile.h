@@ -10,8 +10,8 @@
 // A workgroup owns FT features x TT tokens, its WF x WT wavefronts NF x NT
 // fragments of 16 x 16 each.  Per step 128 bytes of k (64 values of 16 bits, 256
 // of 4) of both tiles are brought into LDS by loads that write LDS themselves,
-// into the half that the step before last used, while the matrix cores work on
-// the other half: one barrier a step, in its middle.
+// into a stage that an earlier step used, while the matrix cores work on another:
+// one barrier a step, in its middle.
 //
 // Bounds.  Every load goes through a buffer descriptor that ends with the
 // operand's last row (the last live token's, where tokens are bounded), so what
@@ -62,6 +62,7 @@ struct TileArgs {
     int32_t F, T, K;                     // K: values; strided operands: rows
     int32_t blocks;                      // MX4: blocks of 32 a row
     const int32_t *live;                 // bounds T, or K where both operands are strided
+    int32_t act;                         // OP_* of the epilogues that have one
     int32_t splits, k_split;             // slices of k (values, a multiple of the step)
     float *partial;                      // EPI_PARTIAL: [splits, T, gated ? 2 F : F]
     void *out;                           // STORE y [T, F]; GATED h [T, F]; BACKWARD dz; QUANTIZE codes
@@ -75,81 +76,91 @@ template <int DT> struct KPerStep { static constexpr int value = DT == DT_MX4 ? 
 // Epilogues of eight consecutive features f .. f + 7 of token t (F is a multiple
 // of eight, so they are all there or none is).
 // ---------------------------------------------------------------------------
-template <int ACT> constexpr bool act_gated() { return ACT != OP_SQUARED_RELU; }
-
-template <int ACT>
-__device__ __forceinline__ float act_of(float x) {
-    if constexpr (ACT == OP_SILU_MUL) return silu(x);
-    else if constexpr (ACT == OP_GELU_TANH_MUL) return gelu_tanh(x);
-    else if constexpr (ACT == OP_GELU_ERF_MUL) return gelu_erf(x);
-    else {
-        const float r = __builtin_fmaxf(x, 0.0f);
-        return r * r;
-    }
-}
-
-template <int ACT>
-__device__ __forceinline__ void slope_of(float x, float &f, float &df) {
-    if constexpr (ACT == OP_SILU_MUL) silu_slope(x, f, df);
-    else if constexpr (ACT == OP_GELU_TANH_MUL) gelu_tanh_slope(x, f, df);
-    else if constexpr (ACT == OP_GELU_ERF_MUL) gelu_erf_slope(x, f, df);
-    else {
-        const float r = __builtin_fmaxf(x, 0.0f);
-        f = r * r;
-        df = 2.0f * r;
-    }
-}
-
 template <int DT>
 __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[8]) {
     oct_store<DT, false>((typename Elem<DT>::storage *)base + at, v, 8);
 }
 
-template <int DT>
-__device__ __forceinline__ void load8(const void *base, int64_t at, float (&v)[8]) {
-    Oct<DT> o;
-    oct_load<DT, false>(o, (const typename Elem<DT>::storage *)base + at, 8);
-    oct_unpack<DT>(o, v);
-}
-
-// act(gate) * up (or act(gate)) of eight features.
-template <int ACT>
-__device__ __forceinline__ void activate8(const float (&g)[8], const float (&u)[8], float (&h)[8]) {
+// act(gate) * up of eight features; PAIR false: the squared ReLU of the gate
+// alone.  EXACT: the erf GELU by the library's erfc, where a value's last bits may
+// decide its 4-bit code, in place of the approximation of absolute error 1.5e-7.
+template <bool PAIR, bool EXACT>
+__device__ __forceinline__ void activate8(int act, const float (&g)[8], const float (&u)[8], float (&h)[8]) {
+    const auto each = [&](auto f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = act_gated<ACT>() ? act_of<ACT>(g[e]) * u[e] : act_of<ACT>(g[e]);
+        for (int e = 0; e < 8; ++e) h[e] = f(g[e]) * u[e];
+    };
+    if constexpr (!PAIR) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float r = __builtin_fmaxf(g[e], 0.0f);
+            h[e] = r * r;
+        }
+    } else if (act == OP_SILU_MUL) {
+        each([](float x) { return silu(x); });
+    } else if (act == OP_GELU_TANH_MUL) {
+        each([](float x) { return gelu_tanh(x); });
+    } else if constexpr (EXACT) {
+        each([](float x) { return 0.5f * x * erfcf(x * -0.70710678118654752f); });
+    } else {
+        each([](float x) { return gelu_erf(x); });
+    }
 }
 
-template <int DT, int ACT>
+// The activation and its slope.
+template <bool PAIR>
+__device__ __forceinline__ void slope8(int act, const float (&g)[8], float (&v)[8], float (&dv)[8]) {
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f(g[e], v[e], dv[e]);
+    };
+    if constexpr (!PAIR) {
+        each([](float x, float &f, float &df) {
+            const float r = __builtin_fmaxf(x, 0.0f);
+            f = r * r;
+            df = 2.0f * r;
+        });
+    } else if (act == OP_SILU_MUL) {
+        each([](float x, float &f, float &df) { silu_slope(x, f, df); });
+    } else if (act == OP_GELU_TANH_MUL) {
+        each([](float x, float &f, float &df) { gelu_tanh_slope(x, f, df); });
+    } else {
+        each([](float x, float &f, float &df) { gelu_erf_slope(x, f, df); });
+    }
+}
+
+template <int DT, bool PAIR>
 __device__ __forceinline__ void gated8(const TileArgs &p, int64_t t, int32_t f, const float (&g)[8], const float (&u)[8]) {
-    constexpr bool GATED = act_gated<ACT>();
+    constexpr bool GATED = PAIR;
     const int64_t F = p.F;
     if (p.out2 != nullptr) {
         store8<DT>(p.out2, t * (GATED ? 2 * F : F) + f, g);
         if constexpr (GATED) store8<DT>(p.out2, t * 2 * F + F + f, u);
     }
     float h[8];
-    activate8<ACT>(g, u, h);
+    activate8<PAIR, false>(p.act, g, u, h);
     store8<DT>(p.out, t * F + f, h);
 }
 
-template <int DT, int ACT>
-__device__ __forceinline__ void backward8(const TileArgs &p, int64_t t, int32_t f, const float (&dh)[8]) {
-    constexpr bool GATED = act_gated<ACT>();
+// zg, zu: the kept gate and up values there.
+template <int DT, bool PAIR>
+__device__ __forceinline__ void backward8(const TileArgs &p, int64_t t, int32_t f, const float (&dh)[8], const Oct<DT> &zg,
+                                          const Oct<DT> &zu) {
+    constexpr bool GATED = PAIR;
     const int64_t F = p.F, at = t * (GATED ? 2 * F : F) + f;
-    float g[8], u[8], h[8], dg[8], du[8];
-    load8<DT>(p.z, at, g);
-    if constexpr (GATED) load8<DT>(p.z, at + F, u);
+    float g[8], u[8], h[8], dg[8], du[8], v[8], dv[8];
+    oct_unpack<DT>(zg, g);
+    if constexpr (GATED) oct_unpack<DT>(zu, u);
+    slope8<PAIR>(p.act, g, v, dv);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        float v, dv;
-        slope_of<ACT>(g[e], v, dv);
         if constexpr (GATED) {
-            h[e] = v * u[e];
-            dg[e] = dh[e] * u[e] * dv;
-            du[e] = dh[e] * v;
+            h[e] = v[e] * u[e];
+            dg[e] = dh[e] * u[e] * dv[e];
+            du[e] = dh[e] * v[e];
         } else {
-            h[e] = v;
-            dg[e] = dh[e] * dv;
+            h[e] = v[e];
+            dg[e] = dh[e] * dv[e];
         }
     }
     store8<DT>(p.out, at, dg);
@@ -172,12 +183,13 @@ __device__ __forceinline__ uint32_t top8(const float (&h)[8]) {
 
 // What an epilogue does with eight features of a token (in: they are there).
 // QUANTIZE: F is a multiple of 32, and the four lanes of a quad hold a block of it.
-template <int EPI, int ACT, int OUT>
+// BACKWARD: zg and zu as backward8 takes them.
+template <int EPI, bool PAIR, int OUT>
 __device__ __forceinline__ void finish8(const TileArgs &p, int64_t t, int32_t f, bool in, const float (&v)[8],
-                                        const float (&u)[8]) {
+                                        const float (&u)[8], const Oct<OUT> &zg = Oct<OUT>(), const Oct<OUT> &zu = Oct<OUT>()) {
     if constexpr (EPI == EPI_QUANTIZE) {
         float h[8];
-        activate8<ACT>(v, u, h);
+        activate8<PAIR, true>(p.act, v, u, h);
         uint32_t top = top8(h);
         top = dpp_umax<0xB1>(top);
         top = dpp_umax<0x4E>(top);
@@ -189,8 +201,8 @@ __device__ __forceinline__ void finish8(const TileArgs &p, int64_t t, int32_t f,
         }
     } else if (in) {
         if constexpr (EPI == EPI_STORE) store_row<OUT>(p, t, f, v);
-        else if constexpr (EPI == EPI_GATED) gated8<OUT, ACT>(p, t, f, v, u);
-        else backward8<OUT, ACT>(p, t, f, v);
+        else if constexpr (EPI == EPI_GATED) gated8<OUT, PAIR>(p, t, f, v, u);
+        else backward8<OUT, PAIR>(p, t, f, v, zg, zu);
     }
 }
 
@@ -267,13 +279,15 @@ __device__ __forceinline__ void settled(f32x4 (&acc)[NF][NT]) {
 // ---------------------------------------------------------------------------
 // The kernel.  AK / BK: the operand is strided.  GATED: A has 2 F rows.
 // ---------------------------------------------------------------------------
-template <int DT_, bool AK_, bool BK_, int WF_, int WT_, int NF_, int NT_> struct Tile {
-    static constexpr int DT = DT_, WF = WF_, WT = WT_, NF = NF_, NT = NT_;
+// STAGES: steps of both tiles in LDS, all but one of them being loaded.
+template <int DT_, bool AK_, bool BK_, int WF_, int WT_, int NF_, int NT_, int STAGES_ = 2> struct Tile {
+    static constexpr int DT = DT_, WF = WF_, WT = WT_, NF = NF_, NT = NT_, STAGES = STAGES_;
     static constexpr bool AK = AK_, BK = BK_;
     static constexpr int W = WF * WT, FT = WF * NF * 16, TT = WT * NT * 16;
     static constexpr int KS = KPerStep<DT>::value;
     static constexpr int LA = FT / 8 / W, LB = TT / 8 / W;  // 1024-byte loads a wavefront and step
     static_assert(LA * 8 * W == FT && LB * 8 * W == TT, "loads");
+    static_assert(STAGES == 2 || STAGES == 4, "stages");
     static_assert(DT != DT_MX4 || (!AK && !BK), "scales");
 };
 
@@ -286,17 +300,20 @@ __device__ __forceinline__ constexpr uint32_t feature_of(uint32_t row) {
                  : row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3);
 }
 
-template <typename C, int EPI, int ACT, int OUT>
+template <typename C, int EPI, bool PAIR, int OUT>
 __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     constexpr int DT = C::DT, W = C::W, FT = C::FT, TT = C::TT, NF = C::NF, NT = C::NT;
     constexpr bool MX = DT == DT_MX4;
-    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE || EPI == EPI_PARTIAL) && act_gated<ACT>() && !C::AK;
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE || EPI == EPI_PARTIAL) && PAIR && !C::AK;
     constexpr int FW = GATED ? FT / 2 : FT;  // features of D a workgroup
 
-    __shared__ __attribute__((aligned(16))) uint8_t a0[FT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t b0[TT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t b1[TT * STEP_BYTES];
+    // Arrays of their own: the compiler then sees that a read of one does not wait for the loads into another.
+    constexpr int S = C::STAGES;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[FT * STEP_BYTES], b0[TT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES], b1[TT * STEP_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[S > 2 ? FT * STEP_BYTES : 16], b2[S > 2 ? TT * STEP_BYTES : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t a3[S > 2 ? FT * STEP_BYTES : 16], b3[S > 2 ? TT * STEP_BYTES : 16];
+    uint8_t *const as[4] = {a0, a1, a2, a3}, *const bs[4] = {b0, b1, b2, b3};
     __shared__ uint4 sc[MX ? 3 * (FT + TT) : 1];  // MX4: a row's scales of two steps, twice, and the last ones
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -353,7 +370,9 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     uint32_t vs = 0;
     const int32_t first_block = kb / MX_BLOCK, blocks = MX ? (ke - kb + MX_BLOCK - 1) / MX_BLOCK : 0;  // of this slice
     if constexpr (MX) {
-        if (wave < FT / 64) {
+        if (wave >= (FT + TT) / 64) {
+            vs = FAR;
+        } else if (wave < FT / 64) {
             const uint32_t row = threadIdx.x;
             vs = feature_of<NF, GATED>(row) * (uint32_t)p.blocks;
             if (GATED && row / 16 % NF >= NF / 2) vs += (uint32_t)p.F * (uint32_t)p.blocks;
@@ -362,7 +381,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
             vs = (threadIdx.x - FT) * (uint32_t)p.blocks;
             ws = window(p.b_scales + (int64_t)t0 * p.blocks, (int64_t)rows_b * p.blocks);
         }
-        vs += first_block;
+        if (wave < (FT + TT) / 64) vs += first_block;
     }
 
     // The loads of step s: where they read (aim), and one of them.
@@ -415,6 +434,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     const auto put_scales = [&](u32x4 v, uint4 *to) {
         const uint32_t lo0 = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u), hi0 = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
         const uint32_t lo1 = __builtin_amdgcn_perm(v.w, v.z, 0x05010400u), hi1 = __builtin_amdgcn_perm(v.w, v.z, 0x07030602u);
+        if (W * 64 > FT + TT && wave >= (FT + TT) / 64) return;
         to[threadIdx.x] = uint4{__builtin_amdgcn_perm(lo1, lo0, 0x05040100u), __builtin_amdgcn_perm(lo1, lo0, 0x07060302u),
                                 __builtin_amdgcn_perm(hi1, hi0, 0x05040100u), __builtin_amdgcn_perm(hi1, hi0, 0x07060302u)};
     };
@@ -488,67 +508,87 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
         }
     };
     const auto read_scales = [&](int32_t w, int (&sa)[NF], int (&sb)[NT]) {
-        const uint32_t *h = reinterpret_cast<const uint32_t *>(sc + (w * 16 + 16 > blocks ? 2 : w & 1) * (FT + TT));
+        // (past the last window that one: zeros are multiplied, and its bytes are scales)
+        const int32_t v = w * 16 < blocks ? w : (blocks - 1) / 16;
+        const uint32_t *h = reinterpret_cast<const uint32_t *>(sc + (v * 16 + 16 > blocks ? 2 : v & 1) * (FT + TT));
 #pragma unroll
         for (int i = 0; i < NF; ++i) sa[i] = h[((wf * NF + i) * 16 + r) * 4 + g];
 #pragma unroll
         for (int j = 0; j < NT; ++j) sb[j] = h[(FT + (wt * NT + j) * 16 + r) * 4 + g];
     };
-    const auto landed = [] {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        __syncthreads();
+    // Waits until at most `most` of the wavefront's loads are on their way and
+    // its reads of LDS are done, and for the others to get there.
+    const auto meet = [](auto most) {
+        constexpr int N = decltype(most)::value;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
     // A step's second fragments are read while its first are multiplied, and the
     // next step's first while its second are: the barrier between has products
-    // queued on either side.  Past it the step's own half of LDS is free for the
-    // loads of the step after the next.  Loads of steps that are not there read
+    // queued on either side.  Past it the step's own stage of LDS is free for the
+    // loads of the step S further on.  Loads of steps that are not there read
     // nothing (their offsets are past the end).
+    constexpr int L = C::LA + C::LB;
+    const std::integral_constant<int, (S - 2) * L> but_last;
+    const std::integral_constant<int, 0> none;
+    const std::true_type loads;
+    const std::false_type no_loads;
     i32x4 fa0[NF], fa1[NF], fb0[NT], fb1[NT];
     int sa[NF], sb[NT];
-    const std::integral_constant<int, 0> first;
-    const std::integral_constant<int, 1> second;
-    const std::integral_constant<int, 2> third;
-    const std::integral_constant<int, 3> fourth;
-    const std::true_type loads;
-    const std::false_type none;
+    u32x4 next{};
     if (steps > 0) {
-        load(0, a0, b0);
         if constexpr (MX) {
-            put_scales(load_scales(0), sc);
+            next = load_scales(0);
             if (blocks % 16 != 0) put_last_scales();
         }
-        landed();
-        load(1, a1, b1);
+#pragma unroll
+        for (int e = 0; e < S - 1; ++e) load(e, as[e], bs[e]);
+        if constexpr (MX) put_scales(next, sc);
+        meet(but_last);
+        load(S - 1, as[S - 1], bs[S - 1]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) fb0[j] = read_b(b0, 0, j);
 #pragma unroll
         for (int i = 0; i < NF; ++i) fa0[i] = read_a(a0, 0, i);
         if constexpr (MX) read_scales(0, sa, sb);
     }
-    for (int32_t s = 0; s + 2 <= steps; s += 2) {
-        u32x4 next{};
+    const auto step = [&](int32_t s, auto place) {
+        constexpr int e = decltype(place)::value, n = (e + 1) % S, ODD = e & 1;
         int na[NF], nb[NT];
-        if constexpr (MX) next = load_scales(s / 2 + 1);
-        phase(fa0, fb0, sa, sb, first, a0, b0, 1, fa1, fb1, none, a0, b0);
-        aim(s + 2);
-        landed();
-        phase(fa1, fb1, sa, sb, second, a1, b1, 0, fa0, fb0, loads, a0, b0);
-        phase(fa0, fb0, sa, sb, third, a1, b1, 1, fa1, fb1, none, a1, b1);
-        if constexpr (MX) put_scales(next, sc + ((s / 2 + 1) & 1) * (FT + TT));
-        aim(s + 3);
-        landed();
-        if constexpr (MX) read_scales(s / 2 + 1, na, nb);
-        phase(fa1, fb1, sa, sb, fourth, a0, b0, 0, fa0, fb0, loads, a1, b1);
-        if constexpr (MX) {
+        if constexpr (MX && !ODD) next = load_scales(s / 2 + 1);
+        phase(fa0, fb0, sa, sb, std::integral_constant<int, 2 * ODD>(), as[e], bs[e], 1, fa1, fb1, no_loads, as[e], bs[e]);
+        if constexpr (MX && ODD) put_scales(next, sc + ((s / 2 + 1) & 1) * (FT + TT));
+        aim(s + S);
+        meet(but_last);
+        if constexpr (MX && ODD) read_scales(s / 2 + 1, na, nb);
+        phase(fa1, fb1, sa, sb, std::integral_constant<int, 2 * ODD + 1>(), as[n], bs[n], 0, fa0, fb0, loads, as[e], bs[e]);
+        if constexpr (MX && ODD) {
 #pragma unroll
             for (int i = 0; i < NF; ++i) sa[i] = na[i];
 #pragma unroll
             for (int j = 0; j < NT; ++j) sb[j] = nb[j];
         }
-    }
-    if (steps & 1) {
-        phase(fa0, fb0, sa, sb, first, a0, b0, 1, fa1, fb1, none, a0, b0);
-        phase(fa1, fb1, sa, sb, second, a0, b0, 1, fa0, fb0, none, a0, b0);
+    };
+    if constexpr (S == 2) {
+        for (int32_t s = 0; s + 2 <= steps; s += 2) {
+            step(s, std::integral_constant<int, 0>());
+            step(s + 1, std::integral_constant<int, 1>());
+        }
+        if (steps & 1) {
+            phase(fa0, fb0, sa, sb, std::integral_constant<int, 0>(), a0, b0, 1, fa1, fb1, no_loads, a0, b0);
+            phase(fa1, fb1, sa, sb, std::integral_constant<int, 1>(), a0, b0, 1, fa0, fb0, no_loads, a0, b0);
+        }
+    } else {
+        // up to three steps of zeros at the end
+        for (int32_t s = 0; s < steps; s += 4) {
+            step(s, std::integral_constant<int, 0>());
+            step(s + 1, std::integral_constant<int, 1>());
+            step(s + 2, std::integral_constant<int, 2>());
+            step(s + 3, std::integral_constant<int, 3>());
+        }
     }
     settled(acc);
 
@@ -558,15 +598,31 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     // next ones.  (Straight from the accumulators the unrolled epilogue spills.)
     // Four results of a lane are 16 bytes of a token's row; chunk c of token t
     // sits in c ^ t % 16, so that 16 tokens' writes fall into all banks.
-    constexpr int SPACE = 2 * (FT + TT) * STEP_BYTES / W;  // a wavefront's
+    constexpr int ARRAYS = FT == TT ? 4 : 1, PER = W / ARRAYS;  // arrays in use, wavefronts an array
+    constexpr int SPACE = FT * STEP_BYTES / PER;
     constexpr int JT = SPACE / (NF * 16 * 16 * 4), CHUNKS = NF * 4;  // chunks a token
-    static_assert(NT % JT == 0 && FT == TT && W % 4 == 0, "the four arrays, shared alike");
-    constexpr int PER = W / 4;  // wavefronts an array
+    static_assert(JT > 0 && NT % JT == 0 && W % ARRAYS == 0, "whole tokens");
     uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == 1 ? b0 : wave / PER == 2 ? a1 : b1) + wave % PER * SPACE;
     constexpr int LANES = CHUNKS / (GATED ? 4 : 2), TOKENS = 64 / LANES;  // lanes a token, tokens a pass
-    const int oct = lane % LANES;
+    constexpr int PASSES = JT * 16 / TOKENS, AHEAD = PASSES < 4 ? PASSES : 4;
+    static_assert(PASSES % AHEAD == 0, "passes");
+    const int oct = lane % LANES, token = lane / LANES;
     const int32_t f = f0 + wf * (LANES * 8) + oct * 8;
-    landed();
+    // BACKWARD: the kept values of four passes are on their way (one at a time they
+    // took most of the epilogue)
+    Oct<OUT> zg[AHEAD], zu[AHEAD];
+    constexpr int64_t ZROW = EPI == EPI_BACKWARD ? (PAIR ? 4 : 2) : 0;  // bytes of z a feature
+    const __amdgpu_buffer_rsrc_t wz = window((const uint8_t *)p.z + t0 * ZROW * p.F, rows_b * ZROW * p.F);
+    const auto fetch = [&](int pass, Oct<OUT> &kg, Oct<OUT> &ku) {
+        if constexpr (EPI == EPI_BACKWARD) {
+            const uint32_t at = (wt * NT * 16 + pass * TOKENS + token) * (uint32_t)(ZROW * p.F) + f * 2;
+            kg = __builtin_bit_cast(Oct<OUT>, __builtin_amdgcn_raw_buffer_load_b128(wz, at, 0, 0));
+            if constexpr (PAIR) ku = __builtin_bit_cast(Oct<OUT>, __builtin_amdgcn_raw_buffer_load_b128(wz, at, 2 * p.F, 0));
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(d, zg[d], zu[d]);
+    meet(none);
 #pragma unroll
     for (int half = 0; half < NT / JT; ++half) {
 #pragma unroll
@@ -579,26 +635,30 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
             }
         }
 #pragma unroll 1
-        for (int pass = 0; pass < JT * 16 / TOKENS; ++pass) {
-            const int tok = pass * TOKENS + lane / LANES;
-            const auto get = [&](int chunk, float (&v)[8]) {
-                const f32x4 lo = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + (chunk ^ (tok & 15))) * 16);
-                const f32x4 hi = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + ((chunk + 1) ^ (tok & 15))) * 16);
+        for (int first = 0; first < PASSES; first += AHEAD) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
-            };
-            float v[8], u[8] = {};
-            get(2 * oct, v);
-            if constexpr (GATED) get(CHUNKS / 2 + 2 * oct, u);
-            const int32_t t = t0 + (wt * NT + half * JT) * 16 + tok;
-            if constexpr (EPI == EPI_PARTIAL) {
-                if (t < T && f < p.F) {
-                    uint32_t *at = (uint32_t *)p.partial + ((int64_t)split * p.T + t) * (GATED ? 2 : 1) * p.F + f;
-                    oct_store<DT_F32, false>(at, v, p.F - f);
-                    if constexpr (GATED) oct_store<DT_F32, false>(at + p.F, u, p.F - f);
+            for (int d = 0; d < AHEAD; ++d) {
+                const int pass = half * PASSES + first + d, tok = (first + d) * TOKENS + token;
+                const auto get = [&](int chunk, float (&v)[8]) {
+                    const f32x4 lo = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + (chunk ^ (tok & 15))) * 16);
+                    const f32x4 hi = *reinterpret_cast<const f32x4 *>(mine + (tok * CHUNKS + ((chunk + 1) ^ (tok & 15))) * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+                };
+                float v[8], u[8] = {};
+                get(2 * oct, v);
+                if constexpr (GATED) get(CHUNKS / 2 + 2 * oct, u);
+                const int32_t t = t0 + wt * NT * 16 + pass * TOKENS + token;
+                if constexpr (EPI == EPI_PARTIAL) {
+                    if (t < T && f < p.F) {
+                        uint32_t *at = (uint32_t *)p.partial + ((int64_t)split * p.T + t) * (GATED ? 2 : 1) * p.F + f;
+                        oct_store<DT_F32, false>(at, v, p.F - f);
+                        if constexpr (GATED) oct_store<DT_F32, false>(at + p.F, u, p.F - f);
+                    }
+                } else {
+                    finish8<EPI, PAIR, OUT>(p, t, f, t < T && f < p.F, v, u, zg[d], zu[d]);
                 }
-            } else {
-                finish8<EPI, ACT, OUT>(p, t, f, t < T && f < p.F, v, u);
+                fetch(pass + AHEAD, zg[d], zu[d]);
             }
         }
     }
@@ -610,50 +670,64 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
 // ---------------------------------------------------------------------------
 constexpr int FINISH_BLOCK = 256;
 
-template <int EPI, int ACT, int OUT>
+template <int EPI, bool PAIR, int OUT>
 __global__ __launch_bounds__(FINISH_BLOCK) void finish_kernel(TileArgs p, bool bound_tokens) {
-    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && act_gated<ACT>();
+    constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
     const int32_t octs = (p.F + 7) / 8;
     const int32_t T = bound_tokens && p.live != nullptr ? clamp_live(p.live, p.T) : p.T;
     const int64_t i = (int64_t)blockIdx.x * FINISH_BLOCK + threadIdx.x;
     const int64_t t = i / octs;
     const int32_t f = (int32_t)(i - t * octs) * 8;
     float v[8] = {}, u[8] = {};
+    Oct<OUT> zg, zu;
     if (t < T) {
         const int64_t row = GATED ? 2 * (int64_t)p.F : p.F;
         const uint32_t *at = (const uint32_t *)p.partial + t * row + f;
-        for (int s = 0; s < p.splits; ++s, at += (int64_t)p.T * row) {
-            Oct<DT_F32> o;
-            float w[8];
-            oct_load<DT_F32, false>(o, at, p.F - f);
-            oct_unpack<DT_F32>(o, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += w[e];
-            if constexpr (GATED) {
-                oct_load<DT_F32, false>(o, at + p.F, p.F - f);
+        if constexpr (EPI == EPI_BACKWARD) {
+            using Z = typename Elem<OUT>::storage;
+            const Z *z = (const Z *)p.z + t * (PAIR ? 2 * (int64_t)p.F : p.F) + f;
+            oct_load<OUT, false>(zg, z, 8);
+            if constexpr (PAIR) oct_load<OUT, false>(zu, z + p.F, 8);
+        }
+        // whole: no row ends within eight features, so the loads have no branch and several are on their way
+        const auto add = [&](auto whole) {
+            const int n = decltype(whole)::value ? 8 : p.F - f;
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s) {
+                Oct<DT_F32> o;
+                float w[8];
+                oct_load<DT_F32, false>(o, at + s * ((int64_t)p.T * row), n);
                 oct_unpack<DT_F32>(o, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] += w[e];
+                for (int e = 0; e < 8; ++e) v[e] += w[e];
+                if constexpr (GATED) {
+                    oct_load<DT_F32, false>(o, at + s * ((int64_t)p.T * row) + p.F, n);
+                    oct_unpack<DT_F32>(o, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] += w[e];
+                }
             }
-        }
+        };
+        if (p.F % 8 == 0) add(std::true_type());
+        else add(std::false_type());
     }
-    finish8<EPI, ACT, OUT>(p, t, f, t < T, v, u);
+    finish8<EPI, PAIR, OUT>(p, t, f, t < T, v, u, zg, zu);
 }
 
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
-template <typename C, int EPI, int ACT, int OUT>
+template <typename C, int EPI, bool PAIR, int OUT>
 hipError_t launch_tile(const TileArgs &p, bool halves, hipStream_t stream) {
     const int64_t fw = halves ? C::FT / 2 : C::FT;
     const int64_t n = ((p.F + fw - 1) / fw) * (((int64_t)p.T + C::TT - 1) / C::TT) * p.splits;
-    return launch_kernel(tile_kernel<C, EPI, ACT, OUT>, dim3((uint32_t)n), dim3(C::W * 64), stream, p);
+    return launch_kernel(tile_kernel<C, EPI, PAIR, OUT>, dim3((uint32_t)n), dim3(C::W * 64), stream, p);
 }
 
-template <int EPI, int ACT, int OUT>
+template <int EPI, bool PAIR, int OUT>
 hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t stream) {
     const int64_t n = ((int64_t)p.T * ((p.F + 7) / 8) + FINISH_BLOCK - 1) / FINISH_BLOCK;
-    return launch_kernel(finish_kernel<EPI, ACT, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
+    return launch_kernel(finish_kernel<EPI, PAIR, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
 }
 
 }  // namespace ga
