@@ -159,20 +159,30 @@ def _mxfp4(q, rows, d, device, what, name):
     if q is None:
         return Mxfp4(torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device),
                      torch.empty((rows, nb), dtype=torch.uint8, device=device), d)
-    if not isinstance(q, Mxfp4) or q.d != d:
-        raise ValueError(f"{name}: {what} must be a Mxfp4 of [{rows}, {d}]")
-    _given(q.codes, (rows, 16 * nb), torch.uint8, device, f"{what}.codes", name)
-    _given(q.scales, (rows, nb), torch.uint8, device, f"{what}.scales", name)
+    if not _is_mxfp4(q) or q.d != d or q.codes.shape[0] != rows or q.codes.device != device:
+        raise ValueError(f"{name}: {what} must be a Mxfp4 of [{rows}, {d}] with contiguous arrays on {device}")
     return q
+
+
+def _is_mxfp4(q):
+    """Whether q is a Mxfp4 whose arrays fit one another."""
+    if not isinstance(q, Mxfp4):
+        return False
+    codes, scales, d = q
+    if (not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor) or not isinstance(d, int) or d < 1
+            or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2):
+        return False
+    nb = -(-d // GA_MXFP4_BLOCK)
+    rows, width = codes.shape
+    return (width == 16 * nb and scales.shape == (rows, nb) and codes.device == scales.device and codes.is_contiguous()
+            and scales.is_contiguous())
 
 
 def _held(q, what, name):
     """A Mxfp4 of the caller's on a GPU, checked: (q, rows, d, device)."""
-    if (not isinstance(q, Mxfp4) or not isinstance(q.codes, torch.Tensor) or not q.codes.is_cuda or q.codes.dim() != 2
-            or not isinstance(q.d, int) or q.d < 1):
-        raise ValueError(f"{name}: {what} must be a Mxfp4 of CUDA (HIP) tensors")
-    rows, device = q.codes.shape[0], q.codes.device
-    return _mxfp4(q, rows, q.d, device, what, name), rows, q.d, device
+    if not _is_mxfp4(q) or not q.codes.is_cuda:
+        raise ValueError(f"{name}: {what} must be a Mxfp4 of contiguous CUDA (HIP) tensors")
+    return q, q.codes.shape[0], q.d, q.codes.device
 
 
 def mxfp4_quantize(x, live_rows=None, out=None):

@@ -23,17 +23,21 @@ constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 //     there and the loads' latency counts (bf16 1001 x 1032 x 4112 27.2 us, 128 x
 //     128 37.4, with two stages 49.4; 1032 x 2056 x 1001 128 x 128 13.9, 128 x 64,
 //     289 of them, 19.8).
-// k is cut where most of the card would idle: into slices of at least eight steps
-// until half of it is busy (bf16 64 x 4096 x 8192, 32 tiles: whole 32.8 us, four
-// slices 16.7, eight 18.5), and in two where one workgroup has 192 steps or more.
+//   64 x 64 for up to 64 tokens, where 256 or fewer are there: the weights are all
+//     the bytes there are, and more units bring them (bf16 64 x 4096 by 2 * 8192,
+//     256 of them, 36.4 us; 128 x 64, 128 of them, 43.4).
+// k is cut where part of the card would idle, into slices of at least eight steps
+// that fill it (bf16 64 x 8192 by 4096, weights from HBM: 128 x 64 in two slices
+// 36.3 us, four 23.1, eight 19.3, sixteen, 512 workgroups, 25.7).
 ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step) {
-    constexpr int64_t CUS = 256, LEAST_STEPS = 8, LONG = 192, MOST_SLICES = 64;
+    constexpr int64_t CUS = 256, LEAST_STEPS = 8, MOST_SLICES = 64;
     const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
     const auto tiles = [&](int64_t features, int64_t tokens) {
         const int64_t fw = halves ? features / 2 : features;
         return ((F + fw - 1) / fw) * ((T + tokens - 1) / tokens);
     };
-    const int64_t big = tiles(256, 256), mid = tiles(128, 128), slim = tiles(128, 64);
+    const int64_t big = tiles(256, 256), mid = tiles(128, 128), slim = tiles(128, 64),
+                  thin = tiles(64, 64);
     int64_t splits = 1;
     ProductPlan p{};
     if (contiguous && T <= PRODUCT_FEW_TOKENS) {
@@ -49,11 +53,10 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool cont
         p.tile = PRODUCT_DEEP;
         p.workgroups = mid;
     } else {
-        p.tile = PRODUCT_SLIM;
-        p.workgroups = slim;
-        splits = slim > 0 ? CUS / 2 / slim : 1;
+        p.tile = T <= 64 && thin <= CUS ? PRODUCT_THIN : PRODUCT_SLIM;
+        p.workgroups = p.tile == PRODUCT_THIN ? thin : slim;
+        splits = p.workgroups > 0 ? CUS / p.workgroups : 1;
         splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
-        if (splits < 2 && 2 * slim <= CUS && steps >= LONG) splits = 2;
         splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
     }
     const int64_t per = (steps + splits - 1) / splits;

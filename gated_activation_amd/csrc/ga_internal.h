@@ -198,10 +198,10 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
 // PRODUCT_FEW_TOKENS tokens, both operands with k contiguous, as a stream of the
 // weights (ga_stream.h); else in tiles (ga_tile.h) of 256 features (half as many
 // where a gate and an up half share a tile) x 256 tokens, 128 x 128 with two or
-// four stages (DEEP), or 128 x 64, these with k in `splits` slices of k_split values
-// whose partial sums a second launch adds (splits * T * F fp32, twice that with two
-// halves).
-enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_FEW };
+// four stages (DEEP), or 128 x 64 or 64 x 64, these with k in `splits` slices of
+// k_split values whose partial sums a second launch adds (splits * T * F fp32, twice
+// that with two halves).
+enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_THIN, PRODUCT_FEW };
 constexpr int64_t PRODUCT_FEW_TOKENS = 16;
 struct ProductPlan {
     int tile, splits;

@@ -191,6 +191,7 @@ hipError_t launch_product(TileArgs p, bool halves, float *partial, hipStream_t s
     using Mid = Tile<DT, AK, BK, 2, 2, 4, 4>;
     using Deep = Tile<DT, AK, BK, 2, 2, 4, 4, 4>;
     using Slim = Tile<DT, AK, BK, 2, 2, 4, 2, 4>;
+    using Thin = Tile<DT, AK, BK, 1, 4, 4, 1, 4>;
     const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, !AK && !BK, KPerStep<DT>::value);
     p.splits = plan.splits;
     p.k_split = plan.k_split;
@@ -199,15 +200,19 @@ hipError_t launch_product(TileArgs p, bool halves, float *partial, hipStream_t s
     case PRODUCT_BIG: return launch_tile<Big, EPI, PAIR, OUT>(p, halves, stream);
     case PRODUCT_MID: return launch_tile<Mid, EPI, PAIR, OUT>(p, halves, stream);
     case PRODUCT_DEEP: return launch_tile<Deep, EPI, PAIR, OUT>(p, halves, stream);
-    case PRODUCT_SLIM: break;
+    case PRODUCT_SLIM:
+    case PRODUCT_THIN: break;
     default:
         if constexpr (!AK && !BK) return launch_few<DT, EPI, PAIR, OUT>(p, stream);
         return hipErrorInvalidValue;
     }
-    if (plan.splits == 1) return launch_tile<Slim, EPI, PAIR, OUT>(p, halves, stream);
+    const bool thin = plan.tile == PRODUCT_THIN;
+    if (plan.splits == 1)
+        return thin ? launch_tile<Thin, EPI, PAIR, OUT>(p, halves, stream) : launch_tile<Slim, EPI, PAIR, OUT>(p, halves, stream);
     // the slices' sums: with two halves only for the epilogues that join them
     constexpr bool JOINS = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
-    const hipError_t e = launch_tile<Slim, EPI_PARTIAL, JOINS, DT_F32>(p, halves, stream);
+    const hipError_t e = thin ? launch_tile<Thin, EPI_PARTIAL, JOINS, DT_F32>(p, halves, stream)
+                              : launch_tile<Slim, EPI_PARTIAL, JOINS, DT_F32>(p, halves, stream);
     return e != hipSuccess ? e : launch_finish<EPI, PAIR, OUT>(p, !BK, stream);
 }
 

@@ -234,9 +234,11 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, void *lds, uint
 }
 
 // Chunk swizzles of strided operands by k row (see above): a read's four rows k % 4.
-template <int NF>
+// A lane's pieces are 8 NF bytes apart: 64 of them, or 32 in rows of 256 or 128 bytes.
+template <int FT, int NF>
 __device__ __forceinline__ uint32_t swizzle_a(uint32_t k) {
-    return NF == 8 ? (k & 3) : (k & 1) | (k & 2) << 2;
+    static_assert(NF == 8 || (NF == 4 && FT <= 128), "chunks within a row");
+    return NF == 8 ? (k & 3) : FT == 64 ? (k >> 1 & 1) : (k & 1) | (k & 2) << 2;
 }
 __device__ __forceinline__ uint32_t swizzle_b(uint32_t k) { return (k & 3) << 1; }
 
@@ -309,10 +311,10 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
 
     // Arrays of their own: the compiler then sees that a read of one does not wait for the loads into another.
     constexpr int S = C::STAGES;
+    constexpr int A4 = S > 2 ? FT * STEP_BYTES : 16, B4 = S > 2 ? TT * STEP_BYTES : 16;
     __shared__ __attribute__((aligned(16))) uint8_t a0[FT * STEP_BYTES], b0[TT * STEP_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES], b1[TT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t a2[S > 2 ? FT * STEP_BYTES : 16], b2[S > 2 ? TT * STEP_BYTES : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t a3[S > 2 ? FT * STEP_BYTES : 16], b3[S > 2 ? TT * STEP_BYTES : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[A4], b2[B4], a3[A4], b3[B4];
     uint8_t *const as[4] = {a0, a1, a2, a3}, *const bs[4] = {b0, b1, b2, b3};
     __shared__ uint4 sc[MX ? 3 * (FT + TT) : 1];  // MX4: a row's scales of two steps, twice, and the last ones
 
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     if constexpr (C::AK) {
         constexpr int CPR = FT / 8, RPI = 64 / CPR;
         const uint32_t k = wave * RPI + lane / CPR;
-        va = k * (uint32_t)p.a_row + ((lane % CPR) ^ swizzle_a<NF>(k)) * 16;
+        va = k * (uint32_t)p.a_row + ((lane % CPR) ^ swizzle_a<FT, NF>(k)) * 16;
     } else {
         const uint32_t row = wave * 8 + (lane >> 3);
         chunk_a = (lane & 7) ^ (row >> 1 & 7);
@@ -475,7 +477,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     const auto read_a = [&](const uint8_t *la, int kk, int i) -> i32x4 {
         if constexpr (C::AK) {
             const uint32_t k = kk * 32 + g * 8 + kr;
-            const uint32_t chunk = ((wf * NF * 16 + q * NF * 4 + i * 4) / 8) ^ swizzle_a<NF>(kr);
+            const uint32_t chunk = ((wf * NF * 16 + q * NF * 4 + i * 4) / 8) ^ swizzle_a<FT, NF>(kr);
             const uint8_t *at = la + k * (FT * 2) + chunk * 16 + (i & 1) * 8;
             const i16x4 lo = read_tr(at), hi = read_tr(at + 4 * FT * 2);
             return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -600,7 +602,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     // sits in c ^ t % 16, so that 16 tokens' writes fall into all banks.
     constexpr int ARRAYS = FT == TT ? 4 : 1, PER = W / ARRAYS;  // arrays in use, wavefronts an array
     constexpr int SPACE = FT * STEP_BYTES / PER;
-    constexpr int JT = SPACE / (NF * 16 * 16 * 4), CHUNKS = NF * 4;  // chunks a token
+    constexpr int MOST = SPACE / (NF * 16 * 16 * 4), JT = MOST < NT ? MOST : NT, CHUNKS = NF * 4;  // chunks a token
     static_assert(JT > 0 && NT % JT == 0 && W % ARRAYS == 0, "whole tokens");
     uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == 1 ? b0 : wave / PER == 2 ? a1 : b1) + wave % PER * SPACE;
     constexpr int LANES = CHUNKS / (GATED ? 4 : 2), TOKENS = 64 / LANES;  // lanes a token, tokens a pass
