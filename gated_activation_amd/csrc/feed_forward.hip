@@ -11,51 +11,77 @@ constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Which tiles, by how many workgroups they make for the 256 compute units.
-//   256 x 256, one workgroup a unit, where their last round is at least 0.76 full:
-//     128 x 128, two a unit, run at 0.75 to 0.78 of their rate (bf16 8192 x 4096 x
-//     16384 1284 and 974 TFLOP/s; 4-bit 4096 x 4096 x 16384 4370 and 3410), and at
-//     288 and 384 large tiles (bf16 12288 x 2 * 768 x 2048 and 12288 x 2048 x 768)
-//     take 86 us against 96 and 43 against 45.
-//   128 x 128 with two stages, two a unit, where there are more than 256 of them
-//     (bf16 4112 x 1032 x 1001 20.4 us; four stages, one a unit, 26.9).
-//   128 x 64 or else 128 x 128 with four stages, one a unit, where 256 or fewer are
-//     there and the loads' latency counts (bf16 1001 x 1032 x 4112 27.2 us, 128 x
-//     128 37.4, with two stages 49.4; 1032 x 2056 x 1001 128 x 128 13.9, 128 x 64,
-//     289 of them, 19.8).
-//   64 x 64 for up to 64 tokens, where 256 or fewer are there: the weights are all
-//     the bytes there are, and more units bring them (bf16 64 x 4096 by 2 * 8192,
-//     256 of them, 36.4 us; 128 x 64, 128 of them, 43.4).
+// Which tiles: those whose rounds on the 256 compute units take the least.  A
+// round is a tile on every unit, or two on every unit, and takes as long as it was
+// measured to, relative to the largest tile's (bf16, k of 2048); where two are on a
+// unit, later rounds follow one another tile by tile, and a little over one round
+// takes as long as 1.55 (128 x 192: 512 tiles 54 us, 704 87, 768 78, 896 98, 1408
+// 152; 128 x 128: 512 41, 768 69, 1280 105):
+//   256 x 256, one a unit                    100  (62 us), 88 with fewer of them
+//   128 x 192, two a unit                     87  (54 us), 60 where one is there
+//   128 x 128, two stages, two a unit         66  (41 us), 55
+//   128 x 128, four stages, one a unit        42  (26 us)
+//   128 x 64, four stages, one a unit         30
+// So the large tiles are taken where they fill their rounds (bf16 8192 x 4096 x
+// 16384 1284 TFLOP/s, 128 x 192 1109, 128 x 128 1102; 4-bit 4096 x 4096 x 16384
+// 4370, 128 x 128 3410), 128 x 192 where they don't (12288 x 2 * 768 x 2048 78 us,
+// 256 x 256 98, 128 x 128 94; 2560 x 2 * 4096 x 2048 98, 102, 105), 128 x 128 for a
+// round of it (1024 x 2 * 4096 x 2048 41 us, 128 x 192 49, 256 x 256 55), and four
+// stages, which cover more of the loads' latency, where one tile a unit is all
+// there is (2048 x 2048 x 4096 40 us, two stages 58; 1001 x 1032 x 4112 128 x 64 28
+// us, 128 x 128 39).  128 x 192 is for 16 bits and contiguous operands: two of them
+// with scales do not fit a unit, a row of 192 strided tokens does not divide a load,
+// and with A strided the compiler moves its sums about while products are pending.
+// For up to 64 tokens the weights are all the bytes there are, and more units bring
+// them: 64 x 64 where 256 or fewer are there (bf16 64 x 4096 by 2 * 8192, 256 of
+// them, 36.4 us; 128 x 64, 128 of them, 43.4).
 // k is cut where part of the card would idle, into slices of at least eight steps
 // that fill it (bf16 64 x 8192 by 4096, weights from HBM: 128 x 64 in two slices
 // 36.3 us, four 23.1, eight 19.3, sixteen, 512 workgroups, 25.7).
-ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step) {
+ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strided, int step) {
     constexpr int64_t CUS = 256, LEAST_STEPS = 8, MOST_SLICES = 64;
     const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
     const auto tiles = [&](int64_t features, int64_t tokens) {
         const int64_t fw = halves ? features / 2 : features;
         return ((F + fw - 1) / fw) * ((T + tokens - 1) / tokens);
     };
-    const int64_t big = tiles(256, 256), mid = tiles(128, 128), slim = tiles(128, 64),
-                  thin = tiles(64, 64);
-    int64_t splits = 1;
     ProductPlan p{};
-    if (contiguous && T <= PRODUCT_FEW_TOKENS) {
+    if (strided == 0 && T <= PRODUCT_FEW_TOKENS) {
         p.tile = PRODUCT_FEW;
         p.workgroups = (F + 7) / 8;  // at most
-    } else if (100 * big >= 76 * CUS * ((big + CUS - 1) / CUS)) {
-        p.tile = PRODUCT_BIG;
-        p.workgroups = big;
-    } else if (mid > CUS) {
-        p.tile = PRODUCT_MID;
-        p.workgroups = mid;
-    } else if (slim > CUS) {
-        p.tile = PRODUCT_DEEP;
-        p.workgroups = mid;
-    } else {
-        p.tile = T <= 64 && thin <= CUS ? PRODUCT_THIN : PRODUCT_SLIM;
-        p.workgroups = p.tile == PRODUCT_THIN ? thin : slim;
-        splits = p.workgroups > 0 ? CUS / p.workgroups : 1;
+        p.splits = 1;
+        p.k_split = INT32_MAX;
+        return p;
+    }
+    // a_unit: tiles of it at a time; part: a round of at most one a unit
+    const struct {
+        int tile;
+        int64_t features, tokens, a_unit, round, part;
+        bool there;
+    } choices[] = {{PRODUCT_BIG, 256, 256, 1, 100, 88, true},
+                   {PRODUCT_WIDE, 128, 192, 2, 87, 60, strided == 0 && step == 64},
+                   {PRODUCT_MID, 128, 128, 2, 66, 55, true},
+                   {PRODUCT_DEEP, 128, 128, 1, 42, 42, true},
+                   {PRODUCT_SLIM, 128, 64, 1, 30, 30, true}};
+    int64_t least = INT64_MAX;
+    for (const auto &c : choices) {
+        const int64_t n = tiles(c.features, c.tokens), slots = c.a_unit * CUS, last = n % slots;
+        const int64_t cost = c.a_unit == 1 ? n / slots * c.round + (last == 0 ? 0 : c.part)
+                             : n <= CUS    ? c.part
+                             : n <= slots  ? c.round
+                                           : (100 * n > 155 * slots ? 100 * n : 155 * slots) * c.round / (100 * slots);
+        if (!c.there || cost >= least) continue;
+        least = cost;
+        p.tile = c.tile;
+        p.workgroups = n;
+    }
+    if (p.tile == PRODUCT_SLIM && T <= 64 && tiles(64, 64) <= CUS) {
+        p.tile = PRODUCT_THIN;
+        p.workgroups = tiles(64, 64);
+    }
+    int64_t splits = 1;
+    if ((p.tile == PRODUCT_SLIM || p.tile == PRODUCT_THIN) && p.workgroups > 0) {
+        splits = CUS / p.workgroups;
         splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
         splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
     }
@@ -70,7 +96,7 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool cont
 FeedForwardSpace feed_forward_space(int64_t rows, int64_t H, int64_t d, int halves) {
     FeedForwardSpace s{};
     s.partial = align256((size_t)rows * d * 2);
-    const size_t a = plan_product(d, rows, H, halves == 2, true, 64).partial_bytes, b = plan_product(H, rows, d, false, true, 64).partial_bytes;
+    const size_t a = plan_product(d, rows, H, halves == 2, 0, 64).partial_bytes, b = plan_product(H, rows, d, false, 0, 64).partial_bytes;
     s.total = s.partial + align256(a > b ? a : b);
     return s;
 }
@@ -79,10 +105,10 @@ FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d,
     FeedForwardSpace s{};
     s.gradient = align256((size_t)rows * d * 2);
     s.partial = s.gradient + align256((size_t)rows * halves * d * 2);
-    const size_t parts[4] = {plan_product(d, rows, H, false, false, 64).partial_bytes,
-                             plan_product(H, rows, halves * d, false, false, 64).partial_bytes,
-                             plan_product(H, halves * d, rows, false, false, 64).partial_bytes,
-                             plan_product(d, H, rows, false, false, 64).partial_bytes};
+    const size_t parts[4] = {plan_product(d, rows, H, false, 1, 64).partial_bytes,
+                             plan_product(H, rows, halves * d, false, 1, 64).partial_bytes,
+                             plan_product(H, halves * d, rows, false, 2, 64).partial_bytes,
+                             plan_product(d, H, rows, false, 2, 64).partial_bytes};
     size_t most = 0;
     for (size_t b : parts) most = b > most ? b : most;
     s.total = s.partial + align256(most);

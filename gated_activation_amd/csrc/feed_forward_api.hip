@@ -47,9 +47,9 @@ ga_status check_workspace(const char *op, const void *workspace, size_t bytes, s
 }
 
 // One product's launch; rows and features are counted a few tiles past their end in 32 bits.
-ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step) {
+ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool halves, int strided, int step) {
     if (T > INT32_MAX - 1024) return fail(GA_EUNSUPPORTED, "%s: %lld rows (at most 2^31 - 1025)", op, (long long)T);
-    return check_items(op, ga::plan_product(F, T, K, halves, contiguous, step).workgroups, kTileThreads);
+    return check_items(op, ga::plan_product(F, T, K, halves, strided, step).workgroups, kTileThreads);
 }
 
 bool layer_sizes(int64_t rows, int64_t H, int64_t d, int32_t activation) {
@@ -100,7 +100,7 @@ ga_status ga_feed_forward(const void *x, const void *w_in, const void *w_down, v
                               {"workspace", workspace, workspace_bytes, 256, true, true}};
     if ((st = check_regions(op, regions)) != GA_OK ||
         (st = check_workspace(op, workspace, workspace_bytes, ga_feed_forward_workspace_bytes(rows, H, d, activation))) != GA_OK ||
-        (st = check_product(op, d, rows, H, zd != d, true, 64)) != GA_OK || (st = check_product(op, H, rows, d, false, true, 64)) != GA_OK)
+        (st = check_product(op, d, rows, H, zd != d, 0, 64)) != GA_OK || (st = check_product(op, H, rows, d, false, 0, 64)) != GA_OK)
         return st;
     if (rows == 0) return GA_OK;
     return ga::launched(op, ga::launch_feed_forward(dtype, op_of(activation), x, w_in, w_down, y, kept, (int32_t)rows,
@@ -133,7 +133,7 @@ ga_status ga_feed_forward_backward(const void *dy, const void *x, const void *ke
     if ((st = check_regions(op, regions)) != GA_OK ||
         (st = check_workspace(op, workspace, workspace_bytes,
                               ga_feed_forward_backward_workspace_bytes(rows, H, d, activation))) != GA_OK ||
-        (st = check_product(op, d, rows, H, false, false, 64)) != GA_OK || (st = check_product(op, H, rows, zd, false, false, 64)) != GA_OK)
+        (st = check_product(op, d, rows, H, false, 1, 64)) != GA_OK || (st = check_product(op, H, rows, zd, false, 1, 64)) != GA_OK)
         return st;
     return ga::launched(op, ga::launch_feed_forward_backward(dtype, op_of(activation), dy, x, kept, w_in, w_down, dx, dw_in,
                                                              dw_down, (int32_t)rows, (int32_t)H, (int32_t)d, live_rows,
@@ -197,7 +197,7 @@ ga_status ga_mxfp4_product(const void *a_codes, const uint8_t *a_scales, const v
                               {"workspace", workspace, workspace_bytes, 256, true, true}};
     if ((st = check_regions(op, regions)) != GA_OK ||
         (st = check_workspace(op, workspace, workspace_bytes, ga_mxfp4_product_workspace_bytes(rows, n, k))) != GA_OK ||
-        (st = check_product(op, n, rows, k, false, true, 256)) != GA_OK)
+        (st = check_product(op, n, rows, k, false, 0, 256)) != GA_OK)
         return st;
     if (rows == 0) return GA_OK;
     return ga::launched(op, ga::launch_mxfp4_product(dtype, a_codes, a_scales, w_codes, w_scales, out, (int32_t)rows,
@@ -229,8 +229,8 @@ ga_status ga_feed_forward_mxfp4(const void *x, const void *w_in_codes, const uin
         (st = check_workspace(op, workspace, workspace_bytes,
                               ga_feed_forward_mxfp4_workspace_bytes(rows, H, d, activation))) != GA_OK ||
         (st = ga::check_blocks(op, rows * ga::blocks_of(H))) != GA_OK ||
-        (st = check_product(op, d, rows, H, zd != d, true, 256)) != GA_OK ||
-        (st = check_product(op, H, rows, d, false, true, 256)) != GA_OK)
+        (st = check_product(op, d, rows, H, zd != d, 0, 256)) != GA_OK ||
+        (st = check_product(op, H, rows, d, false, 0, 256)) != GA_OK)
         return st;
     if (rows == 0) return GA_OK;
     return ga::launched(op, ga::launch_feed_forward_mxfp4(dtype, op_of(activation), x, w_in_codes, w_in_scales, w_down_codes,

@@ -197,11 +197,11 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
 // How one product of F features, T tokens and K values runs: up to
 // PRODUCT_FEW_TOKENS tokens, both operands with k contiguous, as a stream of the
 // weights (ga_stream.h); else in tiles (ga_tile.h) of 256 features (half as many
-// where a gate and an up half share a tile) x 256 tokens, 128 x 128 with two or
-// four stages (DEEP), or 128 x 64 or 64 x 64, these with k in `splits` slices of
+// where a gate and an up half share a tile) x 256 tokens, 128 x 192, 128 x 128
+// with two or four stages (DEEP), or 128 x 64 or 64 x 64, these with k in `splits` slices of
 // k_split values whose partial sums a second launch adds (splits * T * F fp32, twice
 // that with two halves).
-enum : int { PRODUCT_BIG, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_THIN, PRODUCT_FEW };
+enum : int { PRODUCT_BIG, PRODUCT_WIDE, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_THIN, PRODUCT_FEW };
 constexpr int64_t PRODUCT_FEW_TOKENS = 16;
 struct ProductPlan {
     int tile, splits;
@@ -209,9 +209,9 @@ struct ProductPlan {
     int64_t workgroups;
     size_t partial_bytes;
 };
-// contiguous: k is in both operands; step: values of k a step (64 of 16 bits, 256
-// of 4)
-ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, bool contiguous, int step);
+// strided: how many operands have k strided (one: A); step: values of k a step (64
+// of 16 bits, 256 of 4)
+ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strided, int step);
 
 // Bytes of workspace, and where its parts begin.
 struct FeedForwardSpace {

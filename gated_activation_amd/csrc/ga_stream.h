@@ -189,15 +189,19 @@ template <int DT, bool AK, bool BK, int EPI, bool PAIR, int OUT>
 hipError_t launch_product(TileArgs p, bool halves, float *partial, hipStream_t stream) {
     using Big = Tile<DT, AK, BK, 2, 4, 8, 4>;
     using Mid = Tile<DT, AK, BK, 2, 2, 4, 4>;
+    using Wide = Tile<DT, AK, BK, 2, 2, 4, 6>;
     using Deep = Tile<DT, AK, BK, 2, 2, 4, 4, 4>;
     using Slim = Tile<DT, AK, BK, 2, 2, 4, 2, 4>;
     using Thin = Tile<DT, AK, BK, 1, 4, 4, 1, 4>;
-    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, !AK && !BK, KPerStep<DT>::value);
+    const ProductPlan plan = plan_product(p.F, p.T, p.K, halves, AK + BK, KPerStep<DT>::value);
     p.splits = plan.splits;
     p.k_split = plan.k_split;
     p.partial = partial;
     switch (plan.tile) {
     case PRODUCT_BIG: return launch_tile<Big, EPI, PAIR, OUT>(p, halves, stream);
+    case PRODUCT_WIDE:
+        if constexpr (!AK && !BK && DT != DT_MX4) return launch_tile<Wide, EPI, PAIR, OUT>(p, halves, stream);
+        return hipErrorInvalidValue;
     case PRODUCT_MID: return launch_tile<Mid, EPI, PAIR, OUT>(p, halves, stream);
     case PRODUCT_DEEP: return launch_tile<Deep, EPI, PAIR, OUT>(p, halves, stream);
     case PRODUCT_SLIM:

@@ -56,7 +56,7 @@ hipError_t layer_as(int op, const void *x, const void *w_in, const uint8_t *w_in
 }  // namespace
 
 size_t mxfp4_product_space(int64_t rows, int64_t n, int64_t k) {
-    return align256(plan_product(n, rows, k, false, true, STEP).partial_bytes);
+    return align256(plan_product(n, rows, k, false, 0, STEP).partial_bytes);
 }
 
 hipError_t launch_mxfp4_product(int dtype, const void *a, const uint8_t *a_scales, const void *w, const uint8_t *w_scales,
@@ -76,7 +76,7 @@ FeedForward4Space feed_forward_mxfp4_space(int64_t rows, int64_t H, int64_t d, i
     s.h_codes = s.x_scales + align256((size_t)rows * blocks_of(H));
     s.h_scales = s.h_codes + align256((size_t)rows * blocks_of(d) * 16);
     s.partial = s.h_scales + align256((size_t)rows * blocks_of(d));
-    const size_t a = plan_product(d, rows, H, halves == 2, true, STEP).partial_bytes, b = plan_product(H, rows, d, false, true, STEP).partial_bytes;
+    const size_t a = plan_product(d, rows, H, halves == 2, 0, STEP).partial_bytes, b = plan_product(H, rows, d, false, 0, STEP).partial_bytes;
     s.total = s.partial + align256(a > b ? a : b);
     return s;
 }
