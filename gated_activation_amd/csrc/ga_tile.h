@@ -76,9 +76,9 @@ template <int DT> struct KPerStep { static constexpr int value = DT == DT_MX4 ? 
 // Epilogues of eight consecutive features f .. f + 7 of token t (F is a multiple
 // of eight, so they are all there or none is).
 // ---------------------------------------------------------------------------
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[8]) {
-    oct_store<DT, false>((typename Elem<DT>::storage *)base + at, v, 8);
+    oct_store<DT, NT>((typename Elem<DT>::storage *)base + at, v, 8);
 }
 
 // act(gate) * up of eight features; PAIR false: the squared ReLU of the gate
@@ -134,8 +134,11 @@ __device__ __forceinline__ void gated8(const TileArgs &p, int64_t t, int32_t f, 
     constexpr bool GATED = PAIR;
     const int64_t F = p.F;
     if (p.out2 != nullptr) {
-        store8<DT>(p.out2, t * (GATED ? 2 * F : F) + f, g);
-        if constexpr (GATED) store8<DT>(p.out2, t * 2 * F + F + f, u);
+        // Read by the backward pass, after much else: past the caches (16384 x 2048 by
+        // 768, 12288 live: 123 us against 128).  Not so dz and h of the backward pass,
+        // which the next products read (1001 x 1032 by 2056: 82 us, 97 past the caches).
+        store8<DT, true>(p.out2, t * (GATED ? 2 * F : F) + f, g);
+        if constexpr (GATED) store8<DT, true>(p.out2, t * 2 * F + F + f, u);
     }
     float h[8];
     activate8<PAIR, false>(p.act, g, u, h);
