@@ -9,6 +9,25 @@ namespace {
 
 constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+constexpr int64_t CUS = 256;
+
+// The slices of k of a plan of p.workgroups tiles.
+void cut(ProductPlan &p, int64_t F, int64_t T, int64_t K, bool halves, int step) {
+    constexpr int64_t LEAST_STEPS = 8, MOST_SLICES = 64;
+    const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
+    int64_t splits = 1;
+    if ((p.tile == PRODUCT_SLIM || p.tile == PRODUCT_THIN) && p.workgroups > 0) {
+        splits = CUS / p.workgroups;
+        splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
+        splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
+    }
+    const int64_t per = (steps + splits - 1) / splits;
+    p.splits = (int)((steps + per - 1) / per);
+    p.k_split = (int32_t)(p.splits == 1 ? INT32_MAX : per * step);
+    p.workgroups *= p.splits;
+    p.partial_bytes = p.splits == 1 ? 0 : (size_t)p.splits * T * F * (halves ? 8 : 4);
+}
+
 }  // namespace
 
 // Which tiles: those whose rounds on the 256 compute units take the least.  A
@@ -39,8 +58,6 @@ constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // that fill it (bf16 64 x 8192 by 4096, weights from HBM: 128 x 64 in two slices
 // 36.3 us, four 23.1, eight 19.3, sixteen, 512 workgroups, 25.7).
 ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strided, int step) {
-    constexpr int64_t CUS = 256, LEAST_STEPS = 8, MOST_SLICES = 64;
-    const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
     const auto tiles = [&](int64_t features, int64_t tokens) {
         const int64_t fw = halves ? features / 2 : features;
         return ((F + fw - 1) / fw) * ((T + tokens - 1) / tokens);
@@ -79,17 +96,28 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strid
         p.tile = PRODUCT_THIN;
         p.workgroups = tiles(64, 64);
     }
-    int64_t splits = 1;
-    if ((p.tile == PRODUCT_SLIM || p.tile == PRODUCT_THIN) && p.workgroups > 0) {
-        splits = CUS / p.workgroups;
-        splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
-        splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
-    }
-    const int64_t per = (steps + splits - 1) / splits;
-    p.splits = (int)((steps + per - 1) / per);
-    p.k_split = (int32_t)(p.splits == 1 ? INT32_MAX : per * step);
-    p.workgroups *= p.splits;
-    p.partial_bytes = p.splits == 1 ? 0 : (size_t)p.splits * T * F * (halves ? 8 : 4);
+    cut(p, F, T, K, halves, step);
+    return p;
+}
+
+// Together where the card has room for them, which one of them alone would leave
+// idle at its ends (bf16, all four products, rows x H by d: 128 x 512 by 1024 30.6 ->
+// 19.8 us, 1024 x 512 by 2048 53.5 -> 39.0, 1024 x 2048 by 2048, with 512 and 768
+// tiles, 93.7 -> 88.8; but 1024 x 4096 by 1024, with 1024 and 768, 88 -> 92), and the
+// weights' gradients, whose k is not cut here, are short (2048 x 256 by 256 35 -> 32
+// us, 3000 of them 39 -> 45) or would not be cut anyway, up to 4096 rows (2600 x 512
+// by 4096 151 -> 118 us).
+ThreePlan plan_three(int64_t rows, int64_t H, int64_t d, int64_t zd) {
+    const auto tiles = [](int64_t F, int64_t T, int64_t side) { return ((F + side - 1) / side) * ((T + side - 1) / side); };
+    ThreePlan p{};
+    p.x.tile = PRODUCT_THIN;
+    p.x.workgroups = tiles(H, rows, 64);
+    cut(p.x, H, rows, zd, false, 64);
+    p.in = tiles(H, zd, 128);
+    p.down = tiles(d, H, 128);
+    const auto whole = [&](int64_t F, int64_t T) { return plan_product(F, T, rows, false, 2, 64).splits == 1; };
+    p.together = rows > 0 && p.x.workgroups <= 2 * CUS && p.in + p.down <= 3 * CUS &&
+                 (rows <= 2048 || (rows <= 4096 && whole(H, zd) && whole(d, H)));
     return p;
 }
 
@@ -109,7 +137,8 @@ FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d,
                              plan_product(H, rows, halves * d, false, 1, 64).partial_bytes,
                              plan_product(H, halves * d, rows, false, 2, 64).partial_bytes,
                              plan_product(d, H, rows, false, 2, 64).partial_bytes};
-    size_t most = 0;
+    const ThreePlan three = plan_three(rows, H, d, halves * d);
+    size_t most = three.together ? three.x.partial_bytes : 0;
     for (size_t b : parts) most = b > most ? b : most;
     s.total = s.partial + align256(most);
     return s;

@@ -57,28 +57,25 @@ hipError_t backward_as(int act, const void *dy, const void *x, const void *kept,
     const FeedForwardSpace at = feed_forward_backward_space(rows, H, d, PAIR ? 2 : 1);
     void *h = workspace + at.hidden, *dz = workspace + at.gradient;
     float *partial = (float *)(workspace + at.partial);
-    hipError_t e = hipSuccess;
     TileArgs p{};
     if (rows > 0) {
         p.a = w_down, p.a_row = 2 * (int64_t)d, p.b = dy, p.b_row = 2 * (int64_t)H;
         p.F = d, p.T = rows, p.K = H, p.act = act, p.live = live, p.out = dz, p.out2 = h, p.z = kept;
-        e = product<DT, KS, KC, EPI_BACKWARD, PAIR>(p, false, partial, stream);
-        if (e != hipSuccess) return e;
-        p = TileArgs{};
-        p.a = w_in, p.a_row = 2 * (int64_t)H, p.b = dz, p.b_row = 2 * (int64_t)zd;
-        p.F = H, p.T = rows, p.K = zd, p.live = live, p.out = dx;
-        e = product<DT, KS, KC, EPI_STORE, false>(p, false, partial, stream);
+        const hipError_t e = product<DT, KS, KC, EPI_BACKWARD, PAIR>(p, false, partial, stream);
         if (e != hipSuccess) return e;
     }
-    p = TileArgs{};
-    p.a = x, p.a_row = 2 * (int64_t)H, p.b = dz, p.b_row = 2 * (int64_t)zd;
-    p.F = H, p.T = zd, p.K = rows, p.live = live, p.out = dw_in;
-    e = product<DT, KS, KS, EPI_STORE, false>(p, false, partial, stream);
-    if (e != hipSuccess) return e;
-    p = TileArgs{};
-    p.a = h, p.a_row = 2 * (int64_t)d, p.b = dy, p.b_row = 2 * (int64_t)H;
-    p.F = d, p.T = H, p.K = rows, p.live = live, p.out = dw_down;
-    return product<DT, KS, KS, EPI_STORE, false>(p, false, partial, stream);
+    TileArgs px{}, pi{}, pd{};
+    px.a = w_in, px.a_row = 2 * (int64_t)H, px.b = dz, px.b_row = 2 * (int64_t)zd;
+    px.F = H, px.T = rows, px.K = zd, px.live = live, px.out = dx;
+    pi.a = x, pi.a_row = 2 * (int64_t)H, pi.b = dz, pi.b_row = 2 * (int64_t)zd;
+    pi.F = H, pi.T = zd, pi.K = rows, pi.live = live, pi.out = dw_in;
+    pd.a = h, pd.a_row = 2 * (int64_t)d, pd.b = dy, pd.b_row = 2 * (int64_t)H;
+    pd.F = d, pd.T = H, pd.K = rows, pd.live = live, pd.out = dw_down;
+    const ThreePlan three = plan_three(rows, H, d, zd);
+    if (three.together) return launch_three<DT>(px, pi, pd, three, partial, stream);
+    hipError_t e = rows > 0 ? product<DT, KS, KC, EPI_STORE, false>(px, false, partial, stream) : hipSuccess;
+    if (e == hipSuccess) e = product<DT, KS, KS, EPI_STORE, false>(pi, false, partial, stream);
+    return e != hipSuccess ? e : product<DT, KS, KS, EPI_STORE, false>(pd, false, partial, stream);
 }
 
 }  // namespace

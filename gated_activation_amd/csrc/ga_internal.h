@@ -213,6 +213,15 @@ struct ProductPlan {
 // of 16 bits, 256 of 4)
 ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strided, int step);
 
+// The backward pass's dx, dw_in and dw_down: in one launch where together, of x
+// (64 x 64 tiles), in and down (128 x 128) workgroups.
+struct ThreePlan {
+    bool together;
+    ProductPlan x;
+    int64_t in, down;
+};
+ThreePlan plan_three(int64_t rows, int64_t H, int64_t d, int64_t zd);
+
 // Bytes of workspace, and where its parts begin.
 struct FeedForwardSpace {
     size_t hidden, gradient, partial, total;

@@ -305,21 +305,18 @@ __device__ __forceinline__ constexpr uint32_t feature_of(uint32_t row) {
                  : row / (16 * NF) * (16 * NF) + (m >> 2) * (4 * NF) + frag * 4 + (m & 3);
 }
 
+// Workgroup `block` of a product.  as, bs: each stage's LDS, FT and TT rows of
+// STEP_BYTES, in arrays of their own by stage: the compiler then sees that a read of
+// one does not wait for the loads into another.  sc: MX4, a row's scales of two
+// steps, twice, and the last ones.
 template <typename C, int EPI, bool PAIR, int OUT>
-__global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
+__device__ __forceinline__ void tile_body(const TileArgs &p, uint32_t block, uint8_t *const (&as)[4], uint8_t *const (&bs)[4],
+                                          uint4 *sc) {
     constexpr int DT = C::DT, W = C::W, FT = C::FT, TT = C::TT, NF = C::NF, NT = C::NT;
     constexpr bool MX = DT == DT_MX4;
     constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE || EPI == EPI_PARTIAL) && PAIR && !C::AK;
     constexpr int FW = GATED ? FT / 2 : FT;  // features of D a workgroup
-
-    // Arrays of their own: the compiler then sees that a read of one does not wait for the loads into another.
     constexpr int S = C::STAGES;
-    constexpr int A4 = S > 2 ? FT * STEP_BYTES : 16, B4 = S > 2 ? TT * STEP_BYTES : 16;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[FT * STEP_BYTES], b0[TT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t a1[FT * STEP_BYTES], b1[TT * STEP_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t a2[A4], b2[B4], a3[A4], b3[B4];
-    uint8_t *const as[4] = {a0, a1, a2, a3}, *const bs[4] = {b0, b1, b2, b3};
-    __shared__ uint4 sc[MX ? 3 * (FT + TT) : 1];  // MX4: a row's scales of two steps, twice, and the last ones
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, wf = wave / C::WT, wt = wave % C::WT;
@@ -331,7 +328,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     // The live tokens' tiles alone are dealt out, so that every XCD has its share
     // (16384 x 2 * 768 x 2048, 12288 of the tokens live: 115 us with the others' dealt too).
     const uint32_t nf = (uint32_t)((p.F + FW - 1) / FW), nt = (uint32_t)((T + TT - 1) / TT), n = nf * nt;
-    const uint32_t all = nf * (uint32_t)((p.T + TT - 1) / TT), split = blockIdx.x / all, id = blockIdx.x - split * all;
+    const uint32_t all = nf * (uint32_t)((p.T + TT - 1) / TT), split = block / all, id = block - split * all;
     if (id >= n) return;
     uint32_t ft, tt;
     tile_of(id, n, nf, nt, ft, tt);
@@ -557,9 +554,9 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
         meet(but_last);
         load(S - 1, as[S - 1], bs[S - 1]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb0[j] = read_b(b0, 0, j);
+        for (int j = 0; j < NT; ++j) fb0[j] = read_b(bs[0], 0, j);
 #pragma unroll
-        for (int i = 0; i < NF; ++i) fa0[i] = read_a(a0, 0, i);
+        for (int i = 0; i < NF; ++i) fa0[i] = read_a(as[0], 0, i);
         if constexpr (MX) read_scales(0, sa, sb);
     }
     const auto step = [&](int32_t s, auto place) {
@@ -585,8 +582,8 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
             step(s + 1, std::integral_constant<int, 1>());
         }
         if (steps & 1) {
-            phase(fa0, fb0, sa, sb, std::integral_constant<int, 0>(), a0, b0, 1, fa1, fb1, no_loads, a0, b0);
-            phase(fa1, fb1, sa, sb, std::integral_constant<int, 1>(), a0, b0, 1, fa0, fb0, no_loads, a0, b0);
+            phase(fa0, fb0, sa, sb, std::integral_constant<int, 0>(), as[0], bs[0], 1, fa1, fb1, no_loads, as[0], bs[0]);
+            phase(fa1, fb1, sa, sb, std::integral_constant<int, 1>(), as[0], bs[0], 1, fa0, fb0, no_loads, as[0], bs[0]);
         }
     } else {
         // up to three steps of zeros at the end
@@ -609,7 +606,7 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
     constexpr int SPACE = FT * STEP_BYTES / PER;
     constexpr int MOST = SPACE / (NF * 16 * 16 * 4), JT = MOST < NT ? MOST : NT, CHUNKS = NF * 4;  // chunks a token
     static_assert(JT > 0 && NT % JT == 0 && W % ARRAYS == 0, "whole tokens");
-    uint8_t *const mine = (wave / PER == 0 ? a0 : wave / PER == ARRAYS / 2 ? a1 : wave / PER == 1 ? b0 : b1) + wave % PER * SPACE;
+    uint8_t *const mine = (wave / PER == 0 ? as[0] : wave / PER == ARRAYS / 2 ? as[1] : wave / PER == 1 ? bs[0] : bs[1]) + wave % PER * SPACE;
     constexpr int LANES = CHUNKS / (GATED ? 4 : 2), TOKENS = 64 / LANES;  // lanes a token, tokens a pass
     constexpr int PASSES = JT * 16 / TOKENS, AHEAD = PASSES < 4 ? PASSES : 4;
     static_assert(PASSES % AHEAD == 0, "passes");
@@ -668,6 +665,39 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
                 fetch(pass + AHEAD, zg[d], zu[d]);
             }
         }
+    }
+}
+
+template <typename C, int EPI, bool PAIR, int OUT>
+__global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
+    constexpr int A = C::FT * STEP_BYTES, B = C::TT * STEP_BYTES, S = C::STAGES;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A], b0[B], a1[A], b1[B];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[S > 2 ? A : 16], b2[S > 2 ? B : 16], a3[S > 2 ? A : 16], b3[S > 2 ? B : 16];
+    __shared__ uint4 sc[C::DT == DT_MX4 ? 3 * (C::FT + C::TT) : 1];
+    uint8_t *const as[4] = {a0, a1, a2, a3}, *const bs[4] = {b0, b1, b2, b3};
+    tile_body<C, EPI, PAIR, OUT>(p, blockIdx.x, as, bs, sc);
+}
+
+// ---------------------------------------------------------------------------
+// Three products in one launch, where none of them fills the card: x (A strided) in
+// tiles of 64 x 64, in and down (both strided) of 128 x 128.  Both tiles take 64 KB
+// of LDS, so any two are on a unit at a time.
+// ---------------------------------------------------------------------------
+template <int DT, int EPI_X, int OUT_X>
+__global__ __launch_bounds__(256) void three_kernel(TileArgs x, TileArgs in, TileArgs down, uint32_t n_x, uint32_t n_in) {
+    using X = Tile<DT, true, false, 1, 4, 4, 1, 4>;
+    using W = Tile<DT, true, true, 2, 2, 4, 4>;
+    constexpr int HALF = X::FT * STEP_BYTES;
+    static_assert(2 * HALF == W::FT * STEP_BYTES && X::TT == X::FT && W::TT == W::FT, "arrays");
+    __shared__ __attribute__((aligned(16))) uint8_t s0[2 * HALF], s1[2 * HALF], s2[2 * HALF], s3[2 * HALF];
+    if (blockIdx.x < n_x) {
+        uint8_t *const as[4] = {s0, s1, s2, s3}, *const bs[4] = {s0 + HALF, s1 + HALF, s2 + HALF, s3 + HALF};
+        tile_body<X, EPI_X, false, OUT_X>(x, blockIdx.x, as, bs, nullptr);
+    } else {
+        uint8_t *const as[4] = {s0, s2, nullptr, nullptr}, *const bs[4] = {s1, s3, nullptr, nullptr};
+        const uint32_t block = blockIdx.x - n_x;
+        if (block < n_in) tile_body<W, EPI_STORE, false, DT>(in, block, as, bs, nullptr);
+        else tile_body<W, EPI_STORE, false, DT>(down, block - n_in, as, bs, nullptr);
     }
 }
 
@@ -735,6 +765,23 @@ template <int EPI, bool PAIR, int OUT>
 hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t stream) {
     const int64_t n = ((int64_t)p.T * ((p.F + 7) / 8) + FINISH_BLOCK - 1) / FINISH_BLOCK;
     return launch_kernel(finish_kernel<EPI, PAIR, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
+}
+
+// x's k may be cut (plan.x), as a product's of its own.
+template <int DT>
+hipError_t launch_three(TileArgs x, const TileArgs &in, const TileArgs &down, const ThreePlan &plan, float *partial,
+                        hipStream_t stream) {
+    x.splits = plan.x.splits;
+    x.k_split = plan.x.k_split;
+    x.partial = partial;
+    TileArgs in1 = in, down1 = down;
+    in1.splits = down1.splits = 1;
+    in1.k_split = down1.k_split = INT32_MAX;
+    const uint32_t n_x = (uint32_t)plan.x.workgroups, n_in = (uint32_t)plan.in;
+    const dim3 grid(n_x + n_in + (uint32_t)plan.down), block(256);
+    if (x.splits == 1) return launch_kernel(three_kernel<DT, EPI_STORE, DT>, grid, block, stream, x, in1, down1, n_x, n_in);
+    const hipError_t e = launch_kernel(three_kernel<DT, EPI_PARTIAL, DT_F32>, grid, block, stream, x, in1, down1, n_x, n_in);
+    return e != hipSuccess ? e : launch_finish<EPI_STORE, false, DT>(x, true, stream);
 }
 
 }  // namespace ga
