@@ -11,6 +11,8 @@ from ._train import ACTIVATIONS, _call, _like, _live, _matrix, _ptr, _scratch
 
 GA_MXFP4_BLOCK = 32
 
+_Tensor, _uint8 = torch.Tensor, torch.uint8
+
 # Those that need a token's gate and up values alone.
 ELEMENTWISE = tuple(a for a in ACTIVATIONS if a != "gelu_sparse")
 
@@ -155,34 +157,38 @@ def feed_forward_backward(dy, x, kept, w_in, w_down, activation="silu", live_row
 
 def _mxfp4(q, rows, d, device, what, name):
     """q checked, or a new Mxfp4 where it is None."""
-    nb = -(-d // GA_MXFP4_BLOCK)
     if q is None:
+        nb = -(-d // GA_MXFP4_BLOCK)
         return Mxfp4(torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device),
                      torch.empty((rows, nb), dtype=torch.uint8, device=device), d)
-    if not _is_mxfp4(q) or q.d != d or q.codes.shape[0] != rows or q.codes.device != device:
+    if _rows(q) != rows or q.d != d or q.codes.device != device:
         raise ValueError(f"{name}: {what} must be a Mxfp4 of [{rows}, {d}] with contiguous arrays on {device}")
     return q
 
 
-def _is_mxfp4(q):
-    """Whether q is a Mxfp4 whose arrays fit one another."""
+def _rows(q):
+    """The rows of a Mxfp4 whose arrays fit one another and are on a GPU, else -1."""
     if not isinstance(q, Mxfp4):
-        return False
+        return -1
     codes, scales, d = q
-    if (not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor) or not isinstance(d, int) or d < 1
-            or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2):
-        return False
+    if (not isinstance(codes, _Tensor) or not isinstance(scales, _Tensor) or not isinstance(d, int) or d < 1
+            or codes.dtype is not _uint8 or scales.dtype is not _uint8):
+        return -1
     nb = -(-d // GA_MXFP4_BLOCK)
-    rows, width = codes.shape
-    return (width == 16 * nb and scales.shape == (rows, nb) and codes.device == scales.device and codes.is_contiguous()
-            and scales.is_contiguous())
+    shape, index = codes.shape, codes.get_device()
+    if (len(shape) != 2 or shape[1] != 16 * nb or scales.shape != (shape[0], nb) or index < 0
+            or index != scales.get_device() or not codes.is_contiguous() or not scales.is_contiguous()):
+        return -1
+    return shape[0]
 
 
 def _held(q, what, name):
-    """A Mxfp4 of the caller's on a GPU, checked: (q, rows, d, device)."""
-    if not _is_mxfp4(q) or not q.codes.is_cuda:
+    """A Mxfp4 of the caller's, checked: (codes, scales, rows, d, device)."""
+    rows = _rows(q)
+    if rows < 0:
         raise ValueError(f"{name}: {what} must be a Mxfp4 of contiguous CUDA (HIP) tensors")
-    return q, q.codes.shape[0], q.d, q.codes.device
+    codes, scales, d = q
+    return codes, scales, rows, d, codes.device
 
 
 def mxfp4_quantize(x, live_rows=None, out=None):
@@ -204,10 +210,10 @@ def mxfp4_dequantize(q, dtype, live_rows=None, out=None):
     name = "mxfp4_dequantize"
     if dtype not in _TORCH_DTYPE:
         raise ValueError(f"{name}: unsupported dtype {dtype}")
-    q, rows, d, device = _held(q, "q", name)
+    codes, scales, rows, d, device = _held(q, "q", name)
     out = _like(out, (rows, d), dtype, device, "out", name)
     live = _live(live_rows, device, name)
-    _call(lib.ga_mxfp4_dequantize, device, q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), rows, d,
+    _call(lib.ga_mxfp4_dequantize, device, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), rows, d,
           _TORCH_DTYPE[dtype], live)
     return out
 
@@ -238,14 +244,14 @@ def mxfp4_product(a, w, dtype=torch.bfloat16, live_rows=None, out=None, workspac
     name = "mxfp4_product"
     if dtype not in _TORCH_DTYPE:
         raise ValueError(f"{name}: unsupported dtype {dtype}")
-    a, rows, d, device = _held(a, "a", name)
-    w, n, wd, wdevice = _held(w, "w", name)
+    a_codes, a_scales, rows, d, device = _held(a, "a", name)
+    w_codes, w_scales, n, wd, wdevice = _held(w, "w", name)
     if wd != d or wdevice != device or n < 1:
         raise ValueError(f"{name}: w must be a Mxfp4 of [n, {d}] on {device}, got [{n}, {wd}] on {wdevice}")
     out = _like(out, (rows, n), dtype, device, "out", name)
     live = _live(live_rows, device, name)
     ws, ws_bytes, held = _scratch(workspace, lib.ga_mxfp4_product_workspace_bytes(rows, n, d), device, name)
-    _call(lib.ga_mxfp4_product, device, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+    _call(lib.ga_mxfp4_product, device, a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
           out.data_ptr(), rows, n, d, _TORCH_DTYPE[dtype], live, ws, ws_bytes)
     del held
     return out
@@ -264,10 +270,9 @@ def feed_forward_mxfp4(x, w_in, w_down, activation="silu", live_rows=None, out=N
         raise ValueError(f"{name}: bf16 or fp16 only, got {x.dtype}")
     rows, H = x.shape
     device = x.device
-    w_down, h2, d, _ = _held(w_down, "w_down", name)
-    if h2 != H:
-        raise ValueError(f"{name}: w_down must be a Mxfp4 of [{H}, d], got [{h2}, {d}]")
-    _mxfp4(w_down, H, d, device, "w_down", name)
+    down, down_scales, h2, d, down_device = _held(w_down, "w_down", name)
+    if h2 != H or down_device != device:
+        raise ValueError(f"{name}: w_down must be a Mxfp4 of [{H}, d] on {device}, got [{h2}, {d}] on {down_device}")
     if w_in is None:
         raise ValueError(f"{name}: w_in must be a Mxfp4")
     _mxfp4(w_in, _gated(activation) * d, H, device, "w_in", name)
@@ -275,7 +280,7 @@ def feed_forward_mxfp4(x, w_in, w_down, activation="silu", live_rows=None, out=N
     live = _live(live_rows, device, name)
     ws, ws_bytes, held = _scratch(workspace, lib.ga_feed_forward_mxfp4_workspace_bytes(rows, H, d, act), device, name)
     _call(lib.ga_feed_forward_mxfp4, device, x.data_ptr(), w_in.codes.data_ptr(), w_in.scales.data_ptr(),
-          w_down.codes.data_ptr(), w_down.scales.data_ptr(), out.data_ptr(), rows, H, d, _TORCH_DTYPE[x.dtype], act, live, ws,
+          down.data_ptr(), down_scales.data_ptr(), out.data_ptr(), rows, H, d, _TORCH_DTYPE[x.dtype], act, live, ws,
           ws_bytes)
     del held
     return out
