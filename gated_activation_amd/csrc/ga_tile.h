@@ -13,6 +13,13 @@
 // into a stage that an earlier step used, while the matrix cores work on another:
 // one barrier a step, in its middle.
 //
+// What bounds it: from a few thousand tokens on the matrix cores (bf16 8192 x 4096
+// by 16384 the gated product with z kept 1700 us, the plain one 850, 1.3 PFLOP/s:
+// they are busy 72 % of the time, at the clock that the card holds under them; 4-bit
+// 4096 x 4096 by 16384 125 us, 4.4 PFLOP/s of the 6.7 that the instruction alone
+// reaches), with fewer the loads of a round of workgroups (64 x 4096 by 2 * 8192 36
+// us, 3.8 TB/s; 1001 x 2056 by 1032 with the backward epilogue 22 us).
+//
 // Bounds.  Every load goes through a buffer descriptor that ends with the
 // operand's last row (the last live token's, where tokens are bounded), so what
 // lies past it reads as zero and adds nothing; a k past the end of a contiguous
@@ -681,7 +688,9 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
 // ---------------------------------------------------------------------------
 // Three products in one launch, where none of them fills the card: x (A strided) in
 // tiles of 64 x 64, in and down (both strided) of 128 x 128.  Both tiles take 64 KB
-// of LDS, so any two are on a unit at a time.
+// of LDS, so any two are on a unit at a time.  Bound by the loads of steps that few
+// wavefronts wait for (fp16 1001 x 1032 by 2056 47 us, the three one after another
+// 65).
 // ---------------------------------------------------------------------------
 template <int DT, int EPI_X, int OUT_X>
 __global__ __launch_bounds__(256) void three_kernel(TileArgs x, TileArgs in, TileArgs down, uint32_t n_x, uint32_t n_in) {

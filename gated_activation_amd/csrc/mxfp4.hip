@@ -7,7 +7,8 @@
 // All three are bound by HBM: every input byte is read once and every output
 // byte written once.  As in checkpoint.hip work is numbered in groups of 128
 // values of a row, eight to each of 16 lanes; a block of 32 is a quad of lanes,
-// so its maximum is two DPP steps.
+// so its maximum is two DPP steps.  Measured, bf16 4096 x 16384: quantise 31 us,
+// dequantise 30 us (5.5 and 5.7 TB/s), silu straight to 4 bits 48 us (6.3 TB/s).
 #include "ga_internal.h"
 #include "ga_mx.h"
 #include "ga_train.h"
