@@ -15,9 +15,9 @@
 //
 // What bounds it: from a few thousand tokens on the matrix cores (bf16 8192 x 4096
 // by 16384 the gated product with z kept 1700 us, the plain one 850, 1.3 PFLOP/s:
-// they are busy 72 % of the time, at the clock that the card holds under them; 4-bit
-// 4096 x 4096 by 16384 125 us, 4.4 PFLOP/s of the 6.7 that the instruction alone
-// reaches), with fewer the loads of a round of workgroups (64 x 4096 by 2 * 8192 36
+// they are busy 72 % of the time, at the clock that the card holds under them, the
+// rest goes to the barrier of each step; 4-bit 4096 x 4096 by 16384 125 us, 4.4
+// PFLOP/s, 56 %), with fewer the loads of a round of workgroups (64 x 4096 by 2 * 8192 36
 // us, 3.8 TB/s; 1001 x 2056 by 1032 with the backward epilogue 22 us).
 //
 // Bounds.  Every load goes through a buffer descriptor that ends with the
