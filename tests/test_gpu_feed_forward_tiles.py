@@ -153,6 +153,23 @@ def test_4_bits_past_2_to_the_31_elements():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+def test_weights_past_2_to_the_31_bytes(rows):
+    """A weight whose rows repeat: so must the outputs, of a stream of it and of tiles."""
+    n, k, block = 9000 * 1000, 512, 1000
+    a = ga.mxfp4_quantize(values(np.random.default_rng(6), (rows, k), "bf16")[0].cuda())
+    part = ga.mxfp4_quantize(values(np.random.default_rng(7), (block, k), "bf16")[0].cuda())
+    w = ga.Mxfp4(part.codes.repeat(n // block, 1), part.scales.repeat(n // block, 1), k)
+    assert w.codes.numel() > 2 ** 31
+    print("product", flush=True)
+    out = ga.mxfp4_product(a, w, torch.bfloat16).view(rows, -1, block)
+    want, bound = ff.product4(*(ga.mxfp4_dequantize(q, torch.float32).double().cpu().numpy() for q in (a, part)), "bf16")
+    close(out[:, 0].contiguous(), want, bound, "product")
+    assert bool((out == out[:, :1]).all())
+    del out, w
+    torch.cuda.empty_cache()
+
+
 def test_two_streams_at_once():
     """Calls that cut k, on two streams, neither waiting for the other; their scratch memory is their own."""
     rng = np.random.default_rng(8)
