@@ -11,21 +11,23 @@ constexpr size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t CUS = 256;
 
-// The slices of k of a plan of p.workgroups tiles.
-void cut(ProductPlan &p, int64_t F, int64_t T, int64_t K, bool halves, int step) {
-    constexpr int64_t LEAST_STEPS = 8, MOST_SLICES = 64;
-    const int64_t steps = K > 0 ? (K + step - 1) / step : 1;
-    int64_t splits = 1;
-    if ((p.tile == PRODUCT_SLIM || p.tile == PRODUCT_THIN) && p.workgroups > 0) {
-        splits = CUS / p.workgroups;
-        splits = splits < steps / LEAST_STEPS ? splits : steps / LEAST_STEPS;
-        splits = splits < 1 ? 1 : splits > MOST_SLICES ? MOST_SLICES : splits;
-    }
+// A plan of p.workgroups tiles with k in `splits` slices.
+void cut(ProductPlan &p, int64_t F, int64_t T, int64_t steps, int64_t splits, bool halves, int step) {
     const int64_t per = (steps + splits - 1) / splits;
     p.splits = (int)((steps + per - 1) / per);
     p.k_split = (int32_t)(p.splits == 1 ? INT32_MAX : per * step);
     p.workgroups *= p.splits;
     p.partial_bytes = p.splits == 1 ? 0 : (size_t)p.splits * T * F * (halves ? 8 : 4);
+}
+
+int64_t steps_of(int64_t K, int step) { return K > 0 ? (K + step - 1) / step : 1; }
+
+// How many slices of at least eight steps bring `tiles` to `slots`.
+int64_t slices(int64_t tiles, int64_t steps, int64_t slots) {
+    constexpr int64_t LEAST_STEPS = 8, MOST_SLICES = 64;
+    int64_t n = tiles > 0 ? slots / tiles : 1;
+    n = n < steps / LEAST_STEPS ? n : steps / LEAST_STEPS;
+    return n < 1 ? 1 : n > MOST_SLICES ? MOST_SLICES : n;
 }
 
 }  // namespace
@@ -96,28 +98,32 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strid
         p.tile = PRODUCT_THIN;
         p.workgroups = tiles(64, 64);
     }
-    cut(p, F, T, K, halves, step);
+    const int64_t steps = steps_of(K, step);
+    cut(p, F, T, steps, p.tile == PRODUCT_SLIM || p.tile == PRODUCT_THIN ? slices(p.workgroups, steps, CUS) : 1, halves, step);
     return p;
 }
 
 // Together where the card has room for them, which one of them alone would leave
-// idle at its ends (bf16, all four products, rows x H by d: 128 x 512 by 1024 30.6 ->
-// 19.8 us, 1024 x 512 by 2048 53.5 -> 39.0, 1024 x 2048 by 2048, with 512 and 768
-// tiles, 93.7 -> 88.8; but 1024 x 4096 by 1024, with 1024 and 768, 88 -> 92), and the
-// weights' gradients, whose k is not cut here, are short (2048 x 256 by 256 35 -> 32
-// us, 3000 of them 39 -> 45) or would not be cut anyway, up to 4096 rows (2600 x 512
-// by 4096 151 -> 118 us).
+// idle at its ends, the weights' gradients cut into slices that fill it twice and all
+// slices added by one launch (bf16, all four products, rows x H by d: 128 x 512 by
+// 1024 30.6 -> 18.8 us, 1024 x 512 by 2048 53.5 -> 39.0, 2048 x 256 by 256 35 -> 23,
+// 4096 x 256 by 512 49 -> 33, 1024 x 2048 by 2048, with 512 and 768 tiles, 93.7 ->
+// 88.8, 4096 x 1280 by 512, with 1280 and 120, 88.6 -> 74.5; but 1024 x 4096 by 1024,
+// with 1024 and 768, 88 -> 92, and 2048 x 2048 by 1024, with 1024 and 384, 86.5 ->
+// 88.0).
 ThreePlan plan_three(int64_t rows, int64_t H, int64_t d, int64_t zd) {
     const auto tiles = [](int64_t F, int64_t T, int64_t side) { return ((F + side - 1) / side) * ((T + side - 1) / side); };
     ThreePlan p{};
-    p.x.tile = PRODUCT_THIN;
     p.x.workgroups = tiles(H, rows, 64);
-    cut(p.x, H, rows, zd, false, 64);
-    p.in = tiles(H, zd, 128);
-    p.down = tiles(d, H, 128);
-    const auto whole = [&](int64_t F, int64_t T) { return plan_product(F, T, rows, false, 2, 64).splits == 1; };
-    p.together = rows > 0 && p.x.workgroups <= 2 * CUS && p.in + p.down <= 3 * CUS &&
-                 (rows <= 2048 || (rows <= 4096 && whole(H, zd) && whole(d, H)));
+    p.in.workgroups = tiles(H, zd, 128);
+    p.down.workgroups = tiles(d, H, 128);
+    const int64_t w = p.in.workgroups + p.down.workgroups, steps = steps_of(rows, 64);
+    const int64_t splits = slices(w, steps, 2 * CUS);
+    p.together = rows > 0 && ((p.x.workgroups <= 2 * CUS && w <= 3 * CUS) || (p.x.workgroups <= 5 * CUS && w <= CUS));
+    cut(p.x, H, rows, steps_of(zd, 64), slices(p.x.workgroups, steps_of(zd, 64), CUS), false, 64);
+    cut(p.in, H, zd, steps, splits, false, 64);
+    cut(p.down, d, H, steps, splits, false, 64);
+    p.cut_w = p.in.splits > 1;
     return p;
 }
 
@@ -138,7 +144,7 @@ FeedForwardSpace feed_forward_backward_space(int64_t rows, int64_t H, int64_t d,
                              plan_product(H, halves * d, rows, false, 2, 64).partial_bytes,
                              plan_product(d, H, rows, false, 2, 64).partial_bytes};
     const ThreePlan three = plan_three(rows, H, d, halves * d);
-    size_t most = three.together ? three.x.partial_bytes : 0;
+    size_t most = three.together ? three.x.partial_bytes + three.in.partial_bytes + three.down.partial_bytes : 0;
     for (size_t b : parts) most = b > most ? b : most;
     s.total = s.partial + align256(most);
     return s;

@@ -213,12 +213,12 @@ struct ProductPlan {
 // of 16 bits, 256 of 4)
 ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strided, int step);
 
-// The backward pass's dx, dw_in and dw_down: in one launch where together, of x
-// (64 x 64 tiles), in and down (128 x 128) workgroups.
+// The backward pass's dx, dw_in and dw_down: in one launch where together, x in 64 x
+// 64 tiles, in and down in 128 x 128; cut_w: these two with k in slices (with the
+// partial sums of all three one after another).
 struct ThreePlan {
-    bool together;
-    ProductPlan x;
-    int64_t in, down;
+    bool together, cut_w;
+    ProductPlan x, in, down;
 };
 ThreePlan plan_three(int64_t rows, int64_t H, int64_t d, int64_t zd);
 

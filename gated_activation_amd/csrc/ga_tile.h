@@ -692,8 +692,10 @@ __global__ __launch_bounds__(C::W * 64) void tile_kernel(TileArgs p) {
 // wavefronts wait for (fp16 1001 x 1032 by 2056 47 us, the three one after another
 // 65).
 // ---------------------------------------------------------------------------
-template <int DT, int EPI_X, int OUT_X>
+template <int DT, bool CUT_X, bool CUT_W>
 __global__ __launch_bounds__(256) void three_kernel(TileArgs x, TileArgs in, TileArgs down, uint32_t n_x, uint32_t n_in) {
+    constexpr int EPI_X = CUT_X ? EPI_PARTIAL : EPI_STORE, OUT_X = CUT_X ? DT_F32 : DT;
+    constexpr int EPI_W = CUT_W ? EPI_PARTIAL : EPI_STORE, OUT_W = CUT_W ? DT_F32 : DT;
     using X = Tile<DT, true, false, 1, 4, 4, 1, 4>;
     using W = Tile<DT, true, true, 2, 2, 4, 4>;
     constexpr int HALF = X::FT * STEP_BYTES;
@@ -705,8 +707,8 @@ __global__ __launch_bounds__(256) void three_kernel(TileArgs x, TileArgs in, Til
     } else {
         uint8_t *const as[4] = {s0, s2, nullptr, nullptr}, *const bs[4] = {s1, s3, nullptr, nullptr};
         const uint32_t block = blockIdx.x - n_x;
-        if (block < n_in) tile_body<W, EPI_STORE, false, DT>(in, block, as, bs, nullptr);
-        else tile_body<W, EPI_STORE, false, DT>(down, block - n_in, as, bs, nullptr);
+        if (block < n_in) tile_body<W, EPI_W, false, OUT_W>(in, block, as, bs, nullptr);
+        else tile_body<W, EPI_W, false, OUT_W>(down, block - n_in, as, bs, nullptr);
     }
 }
 
@@ -717,11 +719,11 @@ __global__ __launch_bounds__(256) void three_kernel(TileArgs x, TileArgs in, Til
 constexpr int FINISH_BLOCK = 256;
 
 template <int EPI, bool PAIR, int OUT>
-__global__ __launch_bounds__(FINISH_BLOCK) void finish_kernel(TileArgs p, bool bound_tokens) {
+__device__ __forceinline__ void finish_body(const TileArgs &p, bool bound_tokens, uint32_t block) {
     constexpr bool GATED = (EPI == EPI_GATED || EPI == EPI_QUANTIZE) && PAIR;
     const int32_t octs = (p.F + 7) / 8;
     const int32_t T = bound_tokens && p.live != nullptr ? clamp_live(p.live, p.T) : p.T;
-    const int64_t i = (int64_t)blockIdx.x * FINISH_BLOCK + threadIdx.x;
+    const int64_t i = (int64_t)block * FINISH_BLOCK + threadIdx.x;
     const int64_t t = i / octs;
     const int32_t f = (int32_t)(i - t * octs) * 8;
     float v[8] = {}, u[8] = {};
@@ -760,6 +762,22 @@ __global__ __launch_bounds__(FINISH_BLOCK) void finish_kernel(TileArgs p, bool b
     finish8<EPI, PAIR, OUT>(p, t, f, t < T, v, u, zg, zu);
 }
 
+template <int EPI, bool PAIR, int OUT>
+__global__ __launch_bounds__(FINISH_BLOCK) void finish_kernel(TileArgs p, bool bound_tokens) {
+    finish_body<EPI, PAIR, OUT>(p, bound_tokens, blockIdx.x);
+}
+
+// Those of three_kernel's products that were cut: n_x and n_in workgroups of the
+// first two (0: not cut), the third's the rest.
+template <int OUT>
+__global__ __launch_bounds__(FINISH_BLOCK) void finish_three_kernel(TileArgs x, TileArgs in, TileArgs down, uint32_t n_x,
+                                                                    uint32_t n_in) {
+    const uint32_t block = blockIdx.x - n_x;
+    if (blockIdx.x < n_x) finish_body<EPI_STORE, false, OUT>(x, true, blockIdx.x);
+    else if (block < n_in) finish_body<EPI_STORE, false, OUT>(in, false, block);
+    else finish_body<EPI_STORE, false, OUT>(down, false, block - n_in);
+}
+
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
@@ -770,27 +788,38 @@ hipError_t launch_tile(const TileArgs &p, bool halves, hipStream_t stream) {
     return launch_kernel(tile_kernel<C, EPI, PAIR, OUT>, dim3((uint32_t)n), dim3(C::W * 64), stream, p);
 }
 
-template <int EPI, bool PAIR, int OUT>
-hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t stream) {
-    const int64_t n = ((int64_t)p.T * ((p.F + 7) / 8) + FINISH_BLOCK - 1) / FINISH_BLOCK;
-    return launch_kernel(finish_kernel<EPI, PAIR, OUT>, dim3((uint32_t)n), dim3(FINISH_BLOCK), stream, p, bound_tokens);
+inline uint32_t finish_blocks(const TileArgs &p) {
+    return (uint32_t)(((int64_t)p.T * ((p.F + 7) / 8) + FINISH_BLOCK - 1) / FINISH_BLOCK);
 }
 
-// x's k may be cut (plan.x), as a product's of its own.
+template <int EPI, bool PAIR, int OUT>
+hipError_t launch_finish(const TileArgs &p, bool bound_tokens, hipStream_t stream) {
+    return launch_kernel(finish_kernel<EPI, PAIR, OUT>, dim3(finish_blocks(p)), dim3(FINISH_BLOCK), stream, p, bound_tokens);
+}
+
+// Any of the three may be cut, in and down both or neither; a second launch then adds
+// the slices of all of them.
 template <int DT>
-hipError_t launch_three(TileArgs x, const TileArgs &in, const TileArgs &down, const ThreePlan &plan, float *partial,
-                        hipStream_t stream) {
-    x.splits = plan.x.splits;
-    x.k_split = plan.x.k_split;
-    x.partial = partial;
-    TileArgs in1 = in, down1 = down;
-    in1.splits = down1.splits = 1;
-    in1.k_split = down1.k_split = INT32_MAX;
-    const uint32_t n_x = (uint32_t)plan.x.workgroups, n_in = (uint32_t)plan.in;
-    const dim3 grid(n_x + n_in + (uint32_t)plan.down), block(256);
-    if (x.splits == 1) return launch_kernel(three_kernel<DT, EPI_STORE, DT>, grid, block, stream, x, in1, down1, n_x, n_in);
-    const hipError_t e = launch_kernel(three_kernel<DT, EPI_PARTIAL, DT_F32>, grid, block, stream, x, in1, down1, n_x, n_in);
-    return e != hipSuccess ? e : launch_finish<EPI_STORE, false, DT>(x, true, stream);
+hipError_t launch_three(TileArgs x, TileArgs in, TileArgs down, const ThreePlan &plan, float *partial, hipStream_t stream) {
+    const auto take = [&](TileArgs &p, const ProductPlan &q) {
+        p.splits = q.splits;
+        p.k_split = q.k_split;
+        p.partial = partial;
+        partial += q.partial_bytes / 4;
+    };
+    take(x, plan.x);
+    take(in, plan.in);
+    take(down, plan.down);
+    const uint32_t n_x = (uint32_t)plan.x.workgroups, n_in = (uint32_t)plan.in.workgroups;
+    const bool cut_x = x.splits > 1, cut_w = plan.cut_w;
+    const auto kernel = cut_x ? cut_w ? three_kernel<DT, true, true> : three_kernel<DT, true, false>
+                              : cut_w ? three_kernel<DT, false, true> : three_kernel<DT, false, false>;
+    const hipError_t e = launch_kernel(kernel, dim3(n_x + n_in + (uint32_t)plan.down.workgroups), dim3(256), stream, x, in, down,
+                                       n_x, n_in);
+    if (e != hipSuccess || (!cut_x && !cut_w)) return e;
+    const uint32_t f_x = cut_x ? finish_blocks(x) : 0, f_in = cut_w ? finish_blocks(in) : 0;
+    return launch_kernel(finish_three_kernel<DT>, dim3(f_x + f_in + (cut_w ? finish_blocks(down) : 0)), dim3(FINISH_BLOCK),
+                         stream, x, in, down, f_x, f_in);
 }
 
 }  // namespace ga

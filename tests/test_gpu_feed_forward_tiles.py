@@ -26,16 +26,20 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("rows,H,d,act,live", [
     (1500, 64, 5632, "silu", None),            # 128 x 192; cut
     (1500, 64, 5632, "squared_relu", 1200),    # 128 x 192 without a gate
-    (5700, 1536, 64, "gelu", None),            # cut; 128 x 192
+    (5700, 1536, 64, "gelu", None),            # cut; 128 x 192; the gradients' products apart and cut
     (2048, 64, 3584, "silu", 1111),            # 256 x 256
     (4096, 3584, 64, "gelu_tanh", None),       # cut; 256 x 256, also of dx
-    (2200, 2000, 72, "silu", 2199),            # 128 x 128, the three products apart and cut
+    (2200, 2000, 72, "silu", 2199),            # cut; 128 x 192; 1120 tiles of dx
     (64, 2048, 4096, "gelu_tanh", None),       # 64 x 64, cut; 256 x 256 of dw_in
     (500, 64, 4096, "silu", 400),              # 128 x 128 with four stages
     (500, 4096, 64, "gelu", None),             # the three together, none cut
     (50, 64, 8192, "silu", 33),                # 64 x 64 whole; the three together, dx cut in 32
-    (2049, 264, 136, "squared_relu", None),    # just past the rows where they are together
-    (2600, 512, 4096, "silu", 2500),           # together past them, the gradients' k whole
+    (2049, 264, 136, "squared_relu", None),    # the three together, the weights' gradients cut in 4 of 33 steps
+    (2600, 512, 4096, "silu", 2500),           # together, all whole
+    (4096, 72, 64, "gelu", 4001),              # all three cut
+    (16384, 64, 64, "silu", 9000),             # cut in 32, of which some have no live row
+    (9000, 512, 128, "gelu_tanh", None),       # 1128 tiles of dx
+    (1024, 4096, 1024, "silu", None),          # apart
 ])
 def test_forms(rows, H, d, act, live):
     print(f"feed forward {act} {rows}x{H}x{d} live {live}", flush=True)
