@@ -12,12 +12,11 @@ import torch
 
 import feed_forward_ref as ff
 import gated_activation_amd as ga
-import train_ref as ref
 from test_gpu_feed_forward import ACTS, check
 from test_gpu_mxfp4 import _layer, _quantised_normal
 from test_gpu_mxfp4 import test_product as check_product
 from test_gpu_mxfp4 import test_product_live_rows_and_large as check_product_live
-from train_gpu import TYPES, close, values
+from train_gpu import PAD, close, values
 
 pytestmark = pytest.mark.gpu
 
@@ -203,6 +202,28 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(i, j) for i, j in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,H,d", [(4096, 72, 64), (100, 1024, 1024), (40, 512, 4096), (5700, 1536, 64)])
+def test_workspaces_of_cut_products(rows, H, d):
+    """Sums of slices stay within the workspace, and need all that is asked for."""
+    rng = np.random.default_rng(rows)
+    t = {k: values(rng, shape, "bf16", std=std)[0].cuda() for k, shape, std in
+         (("x", (rows, H), 1.0), ("w_in", (2 * d, H), H ** -0.5), ("w_down", (H, d), d ** -0.5), ("dy", (rows, H), 1.0))}
+    y, kept = ga.feed_forward_train(t["x"], t["w_in"], t["w_down"])
+    q_in, q_down = ga.mxfp4_quantize(t["w_in"]), ga.mxfp4_quantize(t["w_down"])
+    calls = [(ga.feed_forward_workspace_bytes, lambda w: (ga.feed_forward(t["x"], t["w_in"], t["w_down"], workspace=w),)),
+             (ga.feed_forward_backward_workspace_bytes,
+              lambda w: ga.feed_forward_backward(t["dy"], t["x"], kept, t["w_in"], t["w_down"], workspace=w)),
+             (ga.feed_forward_mxfp4_workspace_bytes, lambda w: (ga.feed_forward_mxfp4(t["x"], q_in, q_down, workspace=w),))]
+    for bytes_of, call in calls:
+        need, want = bytes_of(rows, H, d), call(None)
+        buf = torch.full((need + 4096,), PAD, dtype=torch.uint8, device="cuda")
+        for a, b in zip(call(buf[:need]), want):
+            assert torch.equal(a, b)
+        assert bool((buf[need:] == PAD).all())
+        with pytest.raises(ga.GaError):
+            call(buf[:need - 1])
 
 
 def test_two_graphs_of_one_workspace():
