@@ -89,7 +89,8 @@ __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[
 }
 
 // act(gate) * up of eight features; PAIR false: the squared ReLU of the gate
-// alone.  EXACT: the erf GELU by the library's erfc, where a value's last bits may
+// alone, of which a NaN stays one: a sum over a row, it stands for all of the row's
+// values, and a 4-bit block's NaN scale for finite ones too.  EXACT: the erf GELU by the library's erfc, where a value's last bits may
 // decide its 4-bit code, in place of the approximation of absolute error 1.5e-7.
 template <bool PAIR, bool EXACT>
 __device__ __forceinline__ void activate8(int act, const float (&g)[8], const float (&u)[8], float (&h)[8]) {
@@ -100,7 +101,7 @@ __device__ __forceinline__ void activate8(int act, const float (&g)[8], const fl
     if constexpr (!PAIR) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float r = __builtin_fmaxf(g[e], 0.0f);
+            const float r = above_zero<true>(g[e]);
             h[e] = r * r;
         }
     } else if (act == OP_SILU_MUL) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void slope8(int act, const float (&g)[8], float (&v)[
     };
     if constexpr (!PAIR) {
         each([](float x, float &f, float &df) {
-            const float r = __builtin_fmaxf(x, 0.0f);
+            const float r = above_zero<true>(x);
             f = r * r;
             df = 2.0f * r;
         });

@@ -501,7 +501,9 @@ ga_status ga_balance_loss_backward(const void *logits, const uint8_t *mask, cons
  * GELU_SPARSE is refused (GA_EUNSUPPORTED): its cutoff is a statistic of the whole
  * row of z (ga_gelu_and_mul_sparse and ga_gelu_and_mul_sparse_down serve it).
  * Sums are fp32 on the matrix cores.  z is rounded only where it is kept, h once,
- * y once.
+ * y once.  A NaN in x, a weight or the kept z reaches every output formed from it:
+ * max(NaN, 0) is NaN here, in the 4-bit layer and in the backward pass (the
+ * activation's own entry points take it as 0).
  *   x       [rows, H], y [rows, H], w_in [zd, H], w_down [H, d] of dtype GA_BF16 or
  *           GA_F16 (GA_F32: GA_EUNSUPPORTED), 16-byte aligned
  *   kept    z in dtype [rows, zd], for the backward pass; NULL: not kept
@@ -552,7 +554,8 @@ ga_status ga_mxfp4_quantize(const void *in, void *codes, uint8_t *scales, int64_
 ga_status ga_mxfp4_dequantize(const void *codes, const uint8_t *scales, void *out, int64_t rows, int64_t d,
                               int32_t dtype, const int32_t *live_rows, ga_stream stream);
 /* A gated activation (GELU_SPARSE: GA_EUNSUPPORTED) of in [rows, 2d] (SQUARED_RELU
- * [rows, d]), the value that the forward-only entry points store, quantised. */
+ * [rows, d]), the value that the forward-only entry points store (for SQUARED_RELU
+ * max(NaN, 0) = 0 among them), quantised. */
 ga_status ga_activation_mxfp4(const void *in, void *codes, uint8_t *scales, int64_t rows, int64_t d, int32_t dtype,
                               int32_t activation, const int32_t *live_rows, ga_stream stream);
 
