@@ -67,21 +67,23 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strid
     ProductPlan p{};
     if (strided == 0 && T <= PRODUCT_FEW_TOKENS) {
         p.tile = PRODUCT_FEW;
-        p.workgroups = (F + 7) / 8;  // at most
+        p.threads = 512;
+        // as launch_stream_tokens has it, with two halves at most (a quarter from nine tokens on)
+        p.workgroups = halves || F < PRODUCT_FEW_WIDE ? (F + 7) / 8 : (F + 15) / 16;
         p.splits = 1;
         p.k_split = INT32_MAX;
         return p;
     }
     // a_unit: tiles of it at a time; part: a round of at most one a unit
     const struct {
-        int tile;
+        int tile, threads;
         int64_t features, tokens, a_unit, round, part;
         bool there;
-    } choices[] = {{PRODUCT_BIG, 256, 256, 1, 100, 88, true},
-                   {PRODUCT_WIDE, 128, 192, 2, 87, 60, strided == 0 && step == 64},
-                   {PRODUCT_MID, 128, 128, 2, 66, 55, true},
-                   {PRODUCT_DEEP, 128, 128, 1, 42, 42, true},
-                   {PRODUCT_SLIM, 128, 64, 1, 30, 30, true}};
+    } choices[] = {{PRODUCT_BIG, 512, 256, 256, 1, 100, 88, true},
+                   {PRODUCT_WIDE, 256, 128, 192, 2, 87, 60, strided == 0 && step == 64},
+                   {PRODUCT_MID, 256, 128, 128, 2, 66, 55, true},
+                   {PRODUCT_DEEP, 256, 128, 128, 1, 42, 42, true},
+                   {PRODUCT_SLIM, 256, 128, 64, 1, 30, 30, true}};
     int64_t least = INT64_MAX;
     for (const auto &c : choices) {
         const int64_t n = tiles(c.features, c.tokens), slots = c.a_unit * CUS, last = n % slots;
@@ -92,6 +94,7 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strid
         if (!c.there || cost >= least) continue;
         least = cost;
         p.tile = c.tile;
+        p.threads = c.threads;
         p.workgroups = n;
     }
     if (p.tile == PRODUCT_SLIM && T <= 64 && tiles(64, 64) <= CUS) {

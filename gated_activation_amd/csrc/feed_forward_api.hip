@@ -6,15 +6,12 @@
 
 namespace {
 
-using ga::check_items;
 using ga::check_regions;
 using ga::check_sizes;
 using ga::elem_size;
 using ga::fail;
 using ga::op_of;
 using ga::Region;
-
-constexpr int64_t kTileThreads = 512;  // of a product's workgroup, at most
 
 int halves_of(int32_t activation) { return activation == GA_ACT_SQUARED_RELU ? 1 : 2; }
 
@@ -46,10 +43,15 @@ ga_status check_workspace(const char *op, const void *workspace, size_t bytes, s
     return GA_OK;
 }
 
-// One product's launch; rows and features are counted a few tiles past their end in 32 bits.
+// One product's launch has fewer than 2^32 work-items; rows and features are counted
+// a few tiles past their end in 32 bits.
 ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool halves, int strided, int step) {
     if (T > INT32_MAX - 1024) return fail(GA_EUNSUPPORTED, "%s: %lld rows (at most 2^31 - 1025)", op, (long long)T);
-    return check_items(op, ga::plan_product(F, T, K, halves, strided, step).workgroups, kTileThreads);
+    const ga::ProductPlan p = ga::plan_product(F, T, K, halves, strided, step);
+    if (p.workgroups * p.threads > (int64_t)UINT32_MAX)
+        return fail(GA_EUNSUPPORTED, "%s: a product of %lld features and %lld rows needs %lld workgroups of %d work-items (2^32 or more)",
+                    op, (long long)F, (long long)T, (long long)p.workgroups, p.threads);
+    return GA_OK;
 }
 
 bool layer_sizes(int64_t rows, int64_t H, int64_t d, int32_t activation) {

@@ -202,9 +202,9 @@ hipError_t launch_balance_backward(int dtype, const void *logits, const uint8_t 
 // k_split values whose partial sums a second launch adds (splits * T * F fp32, twice
 // that with two halves).
 enum : int { PRODUCT_BIG, PRODUCT_WIDE, PRODUCT_MID, PRODUCT_DEEP, PRODUCT_SLIM, PRODUCT_THIN, PRODUCT_FEW };
-constexpr int64_t PRODUCT_FEW_TOKENS = 16;
+constexpr int64_t PRODUCT_FEW_TOKENS = 16, PRODUCT_FEW_WIDE = 4096;  // from so many features on 16 a workgroup
 struct ProductPlan {
-    int tile, splits;
+    int tile, threads, splits;  // threads: of a workgroup
     int32_t k_split;
     int64_t workgroups;
     size_t partial_bytes;

@@ -174,7 +174,7 @@ hipError_t launch_stream_tokens(const TileArgs &p, hipStream_t stream) {
     } else if constexpr (EPI == EPI_GATED && PAIR) {
         return launch_stream<DT, 4, NT, NT == 4 ? 4 : 1, EPI, PAIR, OUT>(p, stream);
     } else {
-        return p.F >= 4096 ? launch_stream<DT, 4, NT, 1, EPI, PAIR, OUT>(p, stream)
+        return p.F >= PRODUCT_FEW_WIDE ? launch_stream<DT, 4, NT, 1, EPI, PAIR, OUT>(p, stream)
                            : launch_stream<DT, 2, NT, 1, EPI, PAIR, OUT>(p, stream);
     }
 }

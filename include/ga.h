@@ -508,8 +508,8 @@ ga_status ga_balance_loss_backward(const void *logits, const uint8_t *mask, cons
  *           GA_F16 (GA_F32: GA_EUNSUPPORTED), 16-byte aligned
  *   kept    z in dtype [rows, zd], for the backward pass; NULL: not kept
  *   H, d    8 .. GA_MAX_D, multiples of 8
- *   rows    0 .. 2^31 - 1; where a launch would have 2^32 work-items or more (about
- *           2^31 * 128 / max(H, d) rows): GA_EUNSUPPORTED
+ *   rows    0 .. 2^31 - 1025; where a launch would have 2^32 work-items or more:
+ *           GA_EUNSUPPORTED (rows * max(H, d) of 2^36 or less has fewer)
  *   workspace  ga_feed_forward_workspace_bytes() bytes, 256-byte aligned, any
  *           content; calls that share one must not overlap in time.
  */
@@ -564,7 +564,9 @@ ga_status ga_activation_mxfp4(const void *in, void *codes, uint8_t *scales, int6
  * rounded once to dtype (any of the three).  A NaN block makes the outputs of its
  * row NaN.
  *   a codes, scales of [rows, k]; w of [n, k]; out [rows, n], any alignment natural
- *   to its type.  1 <= n < 2^31 - 1024, 1 <= k <= GA_MAX_D.
+ *   to its type.  1 <= n < 2^31 - 1024, 1 <= k <= GA_MAX_D.  Where a launch would
+ *   have 2^32 work-items or more: GA_EUNSUPPORTED (up to 16 rows: n above 2^27 - 16;
+ *   more: not where rows * n is 2^37 or less).
  *   workspace  ga_mxfp4_product_workspace_bytes() bytes (may be 0), as above.
  */
 size_t ga_mxfp4_product_workspace_bytes(int64_t rows, int64_t n, int64_t k);
