@@ -63,4 +63,6 @@ from ._feed_forward import (  # noqa: F401
     GA_MXFP4_BLOCK, Mxfp4, feed_forward, feed_forward_train, feed_forward_backward, feed_forward_workspace_bytes,
     feed_forward_backward_workspace_bytes, mxfp4_quantize, mxfp4_dequantize, activation_mxfp4, mxfp4_product,
     mxfp4_product_workspace_bytes, feed_forward_mxfp4, feed_forward_mxfp4_workspace_bytes,
+    ProductPlan, plan_feed_forward, plan_mxfp4_product, GA_PRODUCT_HIDDEN, GA_PRODUCT_OUT, GA_PRODUCT_DHIDDEN,
+    GA_PRODUCT_DX, GA_PRODUCT_DW_IN, GA_PRODUCT_DW_DOWN,
 )

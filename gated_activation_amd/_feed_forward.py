@@ -6,15 +6,27 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import _TORCH_DTYPE, lib
+from ._lib import _TORCH_DTYPE, _check, lib
 from ._train import ACTIVATIONS, _call, _like, _live, _matrix, _ptr, _scratch
 
 GA_MXFP4_BLOCK = 32
+(GA_PRODUCT_HIDDEN, GA_PRODUCT_OUT, GA_PRODUCT_DHIDDEN, GA_PRODUCT_DX, GA_PRODUCT_DW_IN,
+ GA_PRODUCT_DW_DOWN) = range(6)
 
 _Tensor, _uint8 = torch.Tensor, torch.uint8
 
 # Those that need a token's gate and up values alone.
 ELEMENTWISE = tuple(a for a in ACTIVATIONS if a != "gelu_sparse")
+
+
+class ProductPlan(ctypes.Structure):
+    """How one of the layer's products runs."""
+    _fields_ = [("features", ctypes.c_int32), ("tokens", ctypes.c_int32), ("stages", ctypes.c_int32),
+                ("k_step", ctypes.c_int32), ("splits", ctypes.c_int32), ("joint", ctypes.c_int32),
+                ("k_slice", ctypes.c_int64), ("grid", ctypes.c_int64)]
+
+    def as_dict(self):
+        return {k: getattr(self, k) for k, _ in self._fields_}
 
 
 def _bind():
@@ -27,6 +39,8 @@ def _bind():
         "ga_activation_mxfp4": [vp, vp, vp, i64, i64, i32, i32, vp, vp],
         "ga_mxfp4_product": [vp] * 5 + [i64] * 3 + [i32, vp, vp, sz, vp],
         "ga_feed_forward_mxfp4": [vp] * 6 + [i64] * 3 + [i32, i32, vp, vp, sz, vp],
+        "ga_plan_feed_forward": [i64, i64, i64, i32, i32, i32, ctypes.POINTER(ProductPlan)],
+        "ga_plan_mxfp4_product": [i64, i64, i64, ctypes.POINTER(ProductPlan)],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -98,6 +112,21 @@ def feed_forward_mxfp4_workspace_bytes(rows, H, d, activation="silu"):
 
 def mxfp4_product_workspace_bytes(rows, n, d):
     return int(lib.ga_mxfp4_product_workspace_bytes(rows, n, d))
+
+
+def plan_feed_forward(rows, H, d, activation, product, bits=16):
+    """How the product GA_PRODUCT_* of a layer of these sizes runs (host only):
+    feed_forward's and its backward pass's, with bits=4 feed_forward_mxfp4's."""
+    p = ProductPlan()
+    _check(lib.ga_plan_feed_forward(rows, H, d, _activation(activation, "plan_feed_forward"), bits, product, ctypes.byref(p)))
+    return p
+
+
+def plan_mxfp4_product(rows, n, d):
+    """How mxfp4_product of [rows, d] and [n, d] runs (host only)."""
+    p = ProductPlan()
+    _check(lib.ga_plan_mxfp4_product(rows, n, d, ctypes.byref(p)))
+    return p
 
 
 def _forward(name, x, w_in, w_down, activation, live_rows, out, kept, keep, workspace):

@@ -117,6 +117,9 @@ ProductPlan plan_product(int64_t F, int64_t T, int64_t K, bool halves, int strid
 ThreePlan plan_three(int64_t rows, int64_t H, int64_t d, int64_t zd) {
     const auto tiles = [](int64_t F, int64_t T, int64_t side) { return ((F + side - 1) / side) * ((T + side - 1) / side); };
     ThreePlan p{};
+    p.x.tile = PRODUCT_THIN;
+    p.in.tile = p.down.tile = PRODUCT_MID;
+    p.x.threads = p.in.threads = p.down.threads = 256;
     p.x.workgroups = tiles(H, rows, 64);
     p.in.workgroups = tiles(H, zd, 128);
     p.down.workgroups = tiles(d, H, 128);

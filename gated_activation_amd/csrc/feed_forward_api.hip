@@ -54,6 +54,16 @@ ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool ha
     return GA_OK;
 }
 
+void describe(const ga::ProductPlan &p, int64_t K, int step, bool joint, ga_product_plan *out) {
+    static const int32_t shapes[][3] = {{256, 256, 2}, {128, 192, 2}, {128, 128, 2}, {128, 128, 4},
+                                        {128, 64, 4},  {64, 64, 4},   {0, 0, 0}};
+    static_assert(ga::PRODUCT_BIG == 0 && ga::PRODUCT_WIDE == 1 && ga::PRODUCT_MID == 2 && ga::PRODUCT_DEEP == 3 &&
+                      ga::PRODUCT_SLIM == 4 && ga::PRODUCT_THIN == 5 && ga::PRODUCT_FEW == 6,
+                  "shapes");
+    const int32_t *s = shapes[p.tile];
+    *out = ga_product_plan{s[0], s[1], s[2], s[0] == 0 ? 0 : step, p.splits, joint, p.splits == 1 ? K : p.k_split, p.workgroups};
+}
+
 bool layer_sizes(int64_t rows, int64_t H, int64_t d, int32_t activation) {
     return rows >= 1 && rows <= INT32_MAX && H >= 1 && H <= GA_MAX_D && d >= 1 && d <= GA_MAX_D && op_of(activation) >= 0;
 }
@@ -238,6 +248,50 @@ ga_status ga_feed_forward_mxfp4(const void *x, const void *w_in_codes, const uin
     return ga::launched(op, ga::launch_feed_forward_mxfp4(dtype, op_of(activation), x, w_in_codes, w_in_scales, w_down_codes,
                                                           w_down_scales, y, (int32_t)rows, (int32_t)H, (int32_t)d, live_rows,
                                                           (uint8_t *)workspace, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// Planners
+// ---------------------------------------------------------------------------
+ga_status ga_plan_feed_forward(int64_t rows, int64_t H, int64_t d, int32_t activation, int32_t bits, int32_t product,
+                               ga_product_plan *plan) {
+    const char *op = "ga_plan_feed_forward";
+    if (plan == nullptr) return fail(GA_EINVAL, "%s: null plan", op);
+    if (bits != 4 && bits != 16) return fail(GA_EINVAL, "%s: %d bits", op, (int)bits);
+    if (product < GA_PRODUCT_HIDDEN || product > (bits == 4 ? GA_PRODUCT_OUT : GA_PRODUCT_DW_DOWN))
+        return fail(GA_EINVAL, "%s: no product %d in %d bits", op, (int)product, (int)bits);
+    const ga_status st = check_layer(op, rows, H, d, bits == 4 ? GA_MXFP4_BLOCK : 8, GA_BF16, activation);
+    if (st != GA_OK) return st;
+    if (rows < 1) return fail(GA_EINVAL, "%s: no rows", op);
+    const bool pair = halves_of(activation) == 2;
+    const int64_t zd = halves_of(activation) * d;
+    const struct {
+        int64_t F, T, K;
+        bool halves;
+        int strided;
+    } of[] = {{d, rows, H, pair, 0}, {H, rows, d, false, 0}, {d, rows, H, false, 1},
+              {H, rows, zd, false, 1}, {H, zd, rows, false, 2}, {d, H, rows, false, 2}};
+    const auto &p = of[product];
+    const int step = bits == 4 ? 256 : 64;
+    if (product >= GA_PRODUCT_DX) {
+        const ga::ThreePlan three = ga::plan_three(rows, H, d, zd);
+        if (three.together) {
+            describe(product == GA_PRODUCT_DX ? three.x : product == GA_PRODUCT_DW_IN ? three.in : three.down, p.K, step, true, plan);
+            return GA_OK;
+        }
+    }
+    describe(ga::plan_product(p.F, p.T, p.K, p.halves, p.strided, step), p.K, step, false, plan);
+    return GA_OK;
+}
+
+ga_status ga_plan_mxfp4_product(int64_t rows, int64_t n, int64_t k, ga_product_plan *plan) {
+    const char *op = "ga_plan_mxfp4_product";
+    if (plan == nullptr) return fail(GA_EINVAL, "%s: null plan", op);
+    const ga_status st = check_sizes(op, rows, k, GA_MAX_D, GA_BF16);
+    if (st != GA_OK) return st;
+    if (rows < 1 || n < 1 || n > INT32_MAX) return fail(GA_EINVAL, "%s: %lld x %lld outputs", op, (long long)rows, (long long)n);
+    describe(ga::plan_product(n, rows, k, false, 0, 256), k, 256, false, plan);
+    return GA_OK;
 }
 
 }  // extern "C"

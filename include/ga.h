@@ -588,6 +588,32 @@ ga_status ga_feed_forward_mxfp4(const void *x, const void *w_in_codes, const uin
                                 size_t workspace_bytes, ga_stream stream);
 
 /*
+ * Host-only planners of these products (no HIP call, usable without a GPU): how
+ * each would run for these sizes, all rows live.  `product` names one of the
+ * layer's; `bits` is 16, or 4 for ga_feed_forward_mxfp4 (the first two).
+ */
+#define GA_PRODUCT_HIDDEN 0   /* z = x w_in^T, h */
+#define GA_PRODUCT_OUT 1      /* y = h w_down^T */
+#define GA_PRODUCT_DHIDDEN 2  /* dh = dy w_down, dz, h */
+#define GA_PRODUCT_DX 3       /* dx = dz w_in */
+#define GA_PRODUCT_DW_IN 4    /* dw_in = dz^T x */
+#define GA_PRODUCT_DW_DOWN 5  /* dw_down = dy^T h */
+typedef struct {
+    int32_t features; /* rows of A of a workgroup's tile (with a gate and an up half: of both); 0: a
+                         stream of the weights (up to 16 rows, not in the backward pass) */
+    int32_t tokens;   /* rows of B of a tile; 0: a stream */
+    int32_t stages;   /* steps of a tile in LDS; 0: a stream */
+    int32_t k_step;   /* values of k a step; 0: a stream */
+    int32_t splits;   /* slices of k, whose sums a second launch adds; 1: none */
+    int32_t joint;    /* 1: the backward pass's last three products in one launch */
+    int64_t k_slice;  /* values of k a slice, a multiple of k_step; k where there is one */
+    int64_t grid;     /* workgroups of this product (a stream: at most) */
+} ga_product_plan;
+ga_status ga_plan_feed_forward(int64_t rows, int64_t H, int64_t d, int32_t activation, int32_t bits, int32_t product,
+                               ga_product_plan *plan);
+ga_status ga_plan_mxfp4_product(int64_t rows, int64_t n, int64_t k, ga_product_plan *plan);
+
+/*
  * Host-only helper: z = Phi^-1(target_sparsity), the cutoff multiplier for
  * a target fraction of zeros (0.95 -> 1.6448536...).  NaN outside (0, 1).
  * Newton's method on the normal CDF, to full double precision.
