@@ -40,6 +40,9 @@ and in microscaled 4 bits (Mxfp4: codes, scales, d):
     activation_mxfp4(x, activation)                   -> Mxfp4 of the activation's result
     mxfp4_product(a, w, dtype)                        -> a w^T
     feed_forward_mxfp4(x, w_in, w_down, activation)   -> y
+
+How these products run (host only): plan_feed_forward(rows, H, d, activation, product),
+plan_mxfp4_product(rows, n, d) -> ProductPlan
 """
 from ._lib import (  # noqa: F401
     GA_BF16, GA_F16, GA_F32, GA_OK, GA_EINVAL, GA_EUNSUPPORTED, GA_EHIP, GA_MAX_D, GA_ROUND_INTERMEDIATES,

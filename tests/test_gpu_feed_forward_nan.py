@@ -89,3 +89,22 @@ def test_4_bit_layer(rows, H, d, act):
     assert torch.equal(y[:, rest], clean[:, rest]) and bool(y[:, 7].isnan().all())
     q_in.scales[d - 2, H // 32 - 1] = 255
     assert bool(ga.feed_forward_mxfp4(x, q_in, q_down, act).isnan().all())
+
+
+@pytest.mark.parametrize("rows", [1, 30, 500])
+def test_fp16_hidden_values_past_the_type(rows):
+    """h is fp16 between the two products: 65520 rounds to an infinity, 255^2 is a number."""
+    x = torch.zeros(rows, 8, device="cuda").half()
+    x[:, 0], x[:, 1] = 255.0, 1.0
+    w_in, w_down = torch.zeros(8, 8, device="cuda").half(), torch.zeros(8, 8, device="cuda").half()
+    w_in[0, 0], w_in[1, 0], w_in[1, 1] = 1.0, 1.0, 1.0     # z = 255, 256
+    w_down[0, 0], w_down[1, 1] = 2.0 ** -8, 2.0 ** -8
+    w_down[2:, 2:] = 1.0
+    y, kept = ga.feed_forward_train(x, w_in, w_down, "squared_relu")
+    assert bool((kept[:, 0] == 255).all()) and bool((kept[:, 1] == 256).all())
+    assert bool((y[:, 1] == float("inf")).all())
+    # (an infinity times the zeros of the other outputs' weights is NaN)
+    w_down[1, 1] = 0.0
+    w_in[1, 1] = 0.0                                       # z = 255, 255
+    y = ga.feed_forward(x, w_in, w_down, "squared_relu")
+    assert bool((y[:, 0] == torch.tensor(65025.0).half().item() / 256).all()) and bool((y[:, 1:] == 0).all())
