@@ -1,5 +1,7 @@
 // The feed-forward layer's entry points of the C-ABI: argument checks and
 // dispatch.  As in api.hip, every check runs on the host before any HIP call.
+#include <stddef.h>
+
 #include "../../include/ga.h"
 #include "ga_host.h"
 #include "ga_internal.h"
@@ -53,6 +55,8 @@ ga_status check_product(const char *op, int64_t F, int64_t T, int64_t K, bool ha
                     op, (long long)F, (long long)T, (long long)p.workgroups, p.threads);
     return GA_OK;
 }
+
+static_assert(sizeof(ga_product_plan) == 40 && offsetof(ga_product_plan, grid) == 32, "ga_product_plan layout");
 
 void describe(const ga::ProductPlan &p, int64_t K, int step, bool joint, ga_product_plan *out) {
     static const int32_t shapes[][3] = {{256, 256, 2}, {128, 192, 2}, {128, 128, 2}, {128, 128, 4},

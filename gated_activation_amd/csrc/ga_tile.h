@@ -90,8 +90,9 @@ __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[
 
 // act(gate) * up of eight features; PAIR false: the squared ReLU of the gate
 // alone, of which a NaN stays one: a sum over a row, it stands for all of the row's
-// values, and a 4-bit block's NaN scale for finite ones too.  EXACT: the erf GELU by the library's erfc, where a value's last bits may
-// decide its 4-bit code, in place of the approximation of absolute error 1.5e-7.
+// values, and a 4-bit block's NaN scale for finite ones too.  EXACT: the erf GELU by
+// the library's erfc, where a value's last bits may decide its 4-bit code, in place
+// of the approximation of absolute error 1.5e-7.
 template <bool PAIR, bool EXACT>
 __device__ __forceinline__ void activate8(int act, const float (&g)[8], const float (&u)[8], float (&h)[8]) {
     const auto each = [&](auto f) {

@@ -504,9 +504,9 @@ ga_status ga_balance_loss_backward(const void *logits, const uint8_t *mask, cons
  * row of z (ga_gelu_and_mul_sparse and ga_gelu_and_mul_sparse_down serve it).
  * Sums are fp32 on the matrix cores.  z is rounded only where it is kept, h once,
  * y once; in fp16 an |h| (a kept |z|) of 65520 or more is an infinity, for
- * SQUARED_RELU from |z| = 256 on.  A NaN in x, a weight or the kept z reaches every output formed from it:
- * max(NaN, 0) is NaN here, in the 4-bit layer and in the backward pass (the
- * activation's own entry points take it as 0).
+ * SQUARED_RELU from |z| = 256 on.  A NaN in x, a weight or the kept z reaches
+ * every output formed from it: max(NaN, 0) is NaN here, in the 4-bit layer and in
+ * the backward pass (the activation's own entry points take it as 0).
  *   x       [rows, H], y [rows, H], w_in [zd, H], w_down [H, d] of dtype GA_BF16 or
  *           GA_F16 (GA_F32: GA_EUNSUPPORTED), 16-byte aligned
  *   kept    z in dtype [rows, zd], for the backward pass; NULL: not kept
@@ -527,7 +527,8 @@ ga_status ga_feed_forward(const void *x, const void *w_in, const void *w_down, v
  *     dz = dh up act'(gate) | dh act(gate)      (SQUARED_RELU: 2 max(z, 0) dh)
  *     dx = dz w_in,  dw_in = dz^T x,  dw_down = dy^T h,  h formed again from z
  * dh stays in fp32; dz and h are rounded to the type once (in fp16 with the same
- * bound), dx, dw_in and dw_down once.  The weights' gradients sum over the live rows (none: zero).
+ * bound), dx, dw_in and dw_down once.  The weights' gradients sum over the live
+ * rows (none: zero).
  */
 size_t ga_feed_forward_backward_workspace_bytes(int64_t rows, int64_t H, int64_t d, int32_t activation);
 ga_status ga_feed_forward_backward(const void *dy, const void *x, const void *kept, const void *w_in, const void *w_down,
